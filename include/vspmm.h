@@ -489,6 +489,117 @@ vspmm_status vspmm_plan_info(vspmm_matrix h, int64_t width, vspmm_direction dir,
                              int32_t *vec, int32_t *slices_per_wave, int32_t *lds_staged,
                              int32_t *kernel, int32_t *tiles);
 
+/* Products with a selection matrix: a matrix whose rows hold one entry, or a
+ * few, given by its index list alone. A language model's embedding lookup is
+ * such a product (token t's row selects row ids[t] of the table), and so is
+ * the routing of tokens to experts (row p of the experts' input selects the
+ * token that was sorted there) and back (a token's row selects its top_k rows,
+ * with weights). Their gradients are products with the transpose, built by the
+ * stable counting sort that builds this library's other transposes (regridding
+ * page, section "How it is built": counts, then placement in source order), so
+ * every sum below has a fixed order and repeats bit for bit.
+ *
+ * Conventions of these calls, beside those above:
+ *  - Dense rows are of one element type with `width` contiguous elements; row
+ *    r of array x starts at x + r * ld_x elements (ld_x >= 0 for arrays that
+ *    are read; >= width for arrays of two or more rows that are written).
+ *    Elements between width and the next row are left as they were. Rows need
+ *    the alignment of one element only. Written arrays must not overlap any
+ *    other array of the call.
+ *  - Sums and products run in float32 for VSPMM_ELT_F32, _BF16 and _F16 and in
+ *    float64 for VSPMM_ELT_F64, and are rounded once (to nearest even) to the
+ *    type written. Weights are float32 (float64 for VSPMM_ELT_F64).
+ *  - Indices outside their range are legal: such a row of the matrix has no
+ *    entry (padding, or rows and experts held by another device), so it selects
+ *    nothing and its output is zero. Nothing is read or written out of bounds
+ *    for any index.
+ *  - The calls hold no state, allocate nothing, wait for nothing and enqueue
+ *    kernels only, so they can be captured into a graph. ws: device, 256-byte
+ *    aligned, used only by the work of that call; calls that may overlap in
+ *    time need workspaces of their own. */
+typedef enum {
+    VSPMM_ELT_F32 = 0,
+    VSPMM_ELT_F64 = 1,
+    VSPMM_ELT_BF16 = 2,
+    VSPMM_ELT_F16 = 3
+} vspmm_elt;
+typedef enum { VSPMM_INDEX_I32 = 0, VSPMM_INDEX_I64 = 1 } vspmm_index;
+
+/* out[t] = scale * table[ids[t]] for t < n. table: n_rows rows; ids: device
+ * int32[n] or int64[n]; an id outside [0, n_rows) gives a row of zeros; out: n
+ * rows. Errors: _NULL, _DIM (an extent negative or above int32, a stride
+ * negative or, for out, below width), _ENUM, _HIP. */
+vspmm_status vspmm_embed(vspmm_elt elt, int64_t n_rows, int64_t width, const void *table,
+                         int64_t ld_table, vspmm_index index, int64_t n, const void *ids,
+                         double scale, void *out, int64_t ld_out, hipStream_t stream);
+
+/* The gradient of vspmm_embed with respect to the table: for every row v,
+ *   grad[v] = scale * sum of dout[t] over the t with ids[t] = v, t ascending
+ * (accumulate == 0: every row is written, rows no token selects as zeros), or
+ *   grad[v] = grad[v] + that (accumulate != 0: only the rows that tokens select
+ * are read and written). dout: n rows of elt; grad: n_rows rows of grad_elt,
+ * which is elt, or VSPMM_ELT_F32 for a bf16 or f16 elt. The tokens are sorted
+ * by id, and runs of equal ids are summed in pieces that depend only on the ids
+ * and sizes: the result repeats bit for bit. ws: vspmm_embed_grad_workspace_size
+ * bytes (may be NULL when that is 0). Errors: as vspmm_embed, plus _ENUM for
+ * another pair of types and _WORKSPACE; n_rows at most 2^31 - 2. */
+vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows, int64_t width,
+                              vspmm_index index, int64_t n, const void *ids, const void *dout,
+                              int64_t ld_dout, double scale, int32_t accumulate, void *grad,
+                              int64_t ld_grad, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* Workspace bytes of vspmm_embed_grad; elt is dout's type. bytes: host.
+ * Errors: _NULL, _ENUM, _DIM. */
+vspmm_status vspmm_embed_grad_workspace_size(vspmm_elt elt, int64_t n_rows, int64_t width,
+                                             int64_t n, size_t *bytes);
+
+/* The routing of n_tokens tokens to their top_k experts each. experts: device
+ * int32 or int64 [n_tokens, top_k]; slot s = t * top_k + k. The slots are sorted
+ * by expert, stably (equal experts in slot order); slots whose expert is
+ * outside [0, n_experts) are dropped and sort last. Outputs (device):
+ *   order    int32[n_tokens * top_k]: order[p] = the slot of row p;
+ *   position int32[n_tokens, top_k]: position[s] = p, the row of slot s; a
+ *            dropped slot holds ~p (that is -1 - p), p one of the last rows;
+ *   offsets  int32[n_experts + 1]: expert e's rows are [offsets[e],
+ *            offsets[e + 1]), and offsets[n_experts] counts the live rows.
+ * n_experts at most 4096 (_UNSUPPORTED above). ws: vspmm_route_workspace_size
+ * bytes. Errors: _NULL, _DIM (n_tokens * top_k above int32), _ENUM,
+ * _UNSUPPORTED, _WORKSPACE, _HIP. */
+vspmm_status vspmm_route(vspmm_index index, int64_t n_tokens, int64_t top_k, int64_t n_experts,
+                         const void *experts, int32_t *order, int32_t *position, int32_t *offsets,
+                         void *ws, size_t ws_bytes, hipStream_t stream);
+vspmm_status vspmm_route_workspace_size(int64_t n_tokens, int64_t top_k, int64_t n_experts,
+                                        size_t *bytes);
+
+/* rows[position[t, k]] = x[t]: every token copied to its experts' rows. x:
+ * n_tokens rows; rows: n_tokens * top_k rows, all written (a dropped slot's row
+ * as zeros). position as vspmm_route gives it, each row once; an entry naming no
+ * row below n_tokens * top_k is passed over. Errors: _NULL, _DIM, _ENUM, _HIP. */
+vspmm_status vspmm_dispatch(vspmm_elt elt, int64_t n_tokens, int64_t top_k, int64_t width,
+                            const void *x, int64_t ld_x, const int32_t *position, void *rows,
+                            int64_t ld_rows, hipStream_t stream);
+
+/* out[t] = sum over k ascending of weight[t, k] * rows[position[t, k]], dropped
+ * slots left out whatever their weight. weight: device [n_tokens, top_k], or
+ * NULL for ones: that is the gradient of vspmm_dispatch (rows = the gradient of
+ * its rows, out = the gradient of x). rows: n_tokens * top_k rows; out: n_tokens
+ * rows. Errors: as vspmm_dispatch. */
+vspmm_status vspmm_combine(vspmm_elt elt, int64_t n_tokens, int64_t top_k, int64_t width,
+                           const void *rows, int64_t ld_rows, const int32_t *position,
+                           const void *weight, void *out, int64_t ld_out, hipStream_t stream);
+
+/* The gradients of vspmm_combine, given dout (n_tokens rows), in one pass:
+ *   grad_rows[position[t, k]] = weight[t, k] * dout[t],
+ *   grad_weight[t, k] = <dout[t], rows[position[t, k]]>.
+ * A dropped slot's row and weight gradient are zero. grad_rows: n_tokens *
+ * top_k rows; grad_weight: of the weights' type [n_tokens, top_k]. Errors: as
+ * vspmm_dispatch. */
+vspmm_status vspmm_combine_grad(vspmm_elt elt, int64_t n_tokens, int64_t top_k, int64_t width,
+                                const void *dout, int64_t ld_dout, const void *rows,
+                                int64_t ld_rows, const int32_t *position, const void *weight,
+                                void *grad_rows, int64_t ld_grad_rows, void *grad_weight,
+                                hipStream_t stream);
+
 /* A static string naming the status. */
 const char *vspmm_status_string(vspmm_status st);
 

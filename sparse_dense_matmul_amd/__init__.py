@@ -10,6 +10,10 @@ raises ImportError, and a call that the library rejects raises VspmmError.
     out = A @ B          # B: n x w (cuda, float32) -> m x w
     out = B @ A          # B: w x m -> w x n
     A.T                  # the transpose, a VCSC over the same arrays
+
+Products with a selection matrix (embedding lookup, tokens routed to experts
+and back, their gradients) are in :mod:`sparse_dense_matmul_amd.selection` and
+offered here too.
 """
 
 from __future__ import annotations
@@ -19,8 +23,9 @@ import os
 
 import torch
 
-__all__ = ["VcsMatrix", "CsrMatrix", "Schedule", "VspmmError", "assemble_csr", "lib", "LIB_PATH",
-           "EXPORTS"]
+__all__ = ["VcsMatrix", "CsrMatrix", "Schedule", "VspmmError", "assemble_csr", "Routing",
+           "combine", "combine_grad", "dispatch", "dispatch_grad", "embedding", "embedding_grad",
+           "embedding_grad_workspace", "route", "lib", "LIB_PATH", "EXPORTS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvspmm.so")
@@ -69,6 +74,18 @@ EXPORTS = {
                                    ctypes.c_int),
     "vspmm_plan_info": ([_vp, _i64, ctypes.c_int, ctypes.c_int, _P(_i32), _P(_i32), _P(_i32),
                          _P(_i32), _P(_i32), _P(_i32), _P(_i32)], ctypes.c_int),
+    "vspmm_embed": ([_i32, _i64, _i64, _vp, _i64, _i32, _i64, _vp, ctypes.c_double, _vp, _i64,
+                     _vp], ctypes.c_int),
+    "vspmm_embed_grad": ([_i32, _i32, _i64, _i64, _i32, _i64, _vp, _vp, _i64, ctypes.c_double,
+                          _i32, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "vspmm_embed_grad_workspace_size": ([_i32, _i64, _i64, _i64, _P(_sz)], ctypes.c_int),
+    "vspmm_route": ([_i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "vspmm_route_workspace_size": ([_i64, _i64, _i64, _P(_sz)], ctypes.c_int),
+    "vspmm_dispatch": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "vspmm_combine": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp],
+                      ctypes.c_int),
+    "vspmm_combine_grad": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
+                            _vp, _vp], ctypes.c_int),
     "vspmm_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "vspmm_set_view": ([_vp, _i32, _vp, _vp, _i64], ctypes.c_int),
     "vspmm_view_name": ([_i32], ctypes.c_char_p),
@@ -590,3 +607,7 @@ def assemble_csr(role: str, n_out: int, n_in: int, elem_ptr, out_idx, in_idx, we
                                     ws.numel() * ws.element_size(), _stream(dev))
     _check(st, "vspmm_assemble_csr")
     return CsrMatrix.from_arrays((rows, cols), row_ptr, col[:nnz], val[:nnz], **kw)
+
+
+from .selection import (Routing, combine, combine_grad, dispatch, dispatch_grad,  # noqa: E402
+                        embedding, embedding_grad, embedding_grad_workspace, route)

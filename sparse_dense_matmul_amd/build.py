@@ -3,8 +3,8 @@
 Run as ``python -m sparse_dense_matmul_amd.build`` or through
 ``__graft_entry__.build()``. The library lands next to this file, where the
 binding loads it from. Each translation unit (the host code with the layout
-builders, and one per kernel family; the VCS walks once per vector width and
-k_short once per element type) is
+builders, one per kernel family and the selection products; the VCS walks once
+per vector width and k_short once per element type) is
 compiled to an object in parallel under ``_build/``, then the objects are
 linked into the library.
 """
@@ -20,6 +20,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+# the selection products (embedding, routing), beside the walks' sources
+SELECT = os.path.join("..", "csrc_select", "select.hip")
 LIB = os.path.join(HERE, "libvspmm.so")
 # the benchmark's ceiling probes (not part of the product library)
 PROBE_LIB = os.path.join(HERE, "libvspmm_probe.so")
@@ -33,6 +35,7 @@ UNITS = [
     ("walk_long.hip", [], "walk_long"),
     ("walk_plain.hip", [], "walk_plain"),
     ("walk_scatter.hip", [], "walk_scatter"),
+    (SELECT, [], "select"),
 ] + [(f"walk_vcs_{kind}.hip", [f"-DVSPMM_VEC={v}"], f"walk_vcs_{kind}_v{v}")
      for kind in ("rows", "long") for v in (1, 2, 4)]
 ARCH = "gfx950"
