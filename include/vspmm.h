@@ -504,7 +504,8 @@ vspmm_status vspmm_plan_info(vspmm_matrix h, int64_t width, vspmm_direction dir,
  *    r of array x starts at x + r * ld_x elements (ld_x >= 0 for arrays that
  *    are read; >= width for arrays of two or more rows that are written).
  *    Elements between width and the next row are left as they were. Rows need
- *    the alignment of one element only. Written arrays must not overlap any
+ *    the alignment of one element only, and hold at most 2^24 elements
+ *    (VSPMM_ERR_UNSUPPORTED above). Written arrays must not overlap any
  *    other array of the call.
  *  - Sums and products run in float32 for VSPMM_ELT_F32, _BF16 and _F16 and in
  *    float64 for VSPMM_ELT_F64, and are rounded once (to nearest even) to the

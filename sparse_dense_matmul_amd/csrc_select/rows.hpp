@@ -1,9 +1,12 @@
 // Dense rows of 16-, 32- and 64-bit elements for the selection products: a
 // row is cut into 16-byte chunks, a lane takes whole chunks, and arithmetic
 // runs in float (double for double elements) with one rounding on the way
-// out. Chunks are loaded at the element's own alignment (gfx950 serves
-// unaligned global accesses of 16 bytes), so odd widths, row strides and
-// offset views take the same path as aligned ones.
+// out. Chunks are loaded and stored at the element's own alignment (gfx950
+// serves unaligned global accesses of 16 bytes), so odd widths, row strides
+// and offset views take the same path as aligned ones. A row whose width is no
+// multiple of the chunk ends in a chunk moved left to end with the row: its
+// first elements are the chunk before's last ones, computed and written twice
+// with the same value. Rows shorter than a chunk go element by element (C = 1).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -26,33 +29,25 @@ struct Sum<double> {
 template <typename T>
 constexpr int kChunk = int(16 / sizeof(T));  // elements per 16-byte chunk
 
-template <typename T>
-using ChunkOf = T __attribute__((ext_vector_type(16 / sizeof(T))));
-// the same, at the alignment of one element
-template <typename T>
-using LooseChunk = T __attribute__((ext_vector_type(16 / sizeof(T)), aligned(alignof(T))));
+// C elements at the alignment of one.
+template <typename T, int C>
+using Vec = T __attribute__((ext_vector_type(C), aligned(alignof(T))));
 
-// N elements at p as one access, or the first `live` of them one by one (the
-// rest zero): a row's last chunk may be cut by the row's end.
-template <typename T>
-__device__ __forceinline__ ChunkOf<T> load_chunk(const T *p, int live = kChunk<T>) {
-    if (live >= kChunk<T>) return *reinterpret_cast<const LooseChunk<T> *>(p);
-    ChunkOf<T> v{};
-#pragma unroll
-    for (int i = 0; i < kChunk<T>; ++i)
-        if (i < live) v[i] = p[i];
-    return v;
+template <int C, typename T>
+__device__ __forceinline__ Vec<T, C> load_vec(const T *p) {
+    return *reinterpret_cast<const Vec<T, C> *>(p);
+}
+template <int C, typename T>
+__device__ __forceinline__ void store_vec(T *p, Vec<T, C> v) {
+    *reinterpret_cast<Vec<T, C> *>(p) = v;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_chunk(T *p, ChunkOf<T> v, int live = kChunk<T>) {
-    if (live >= kChunk<T>) {
-        *reinterpret_cast<LooseChunk<T> *>(p) = v;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < kChunk<T>; ++i)
-        if (i < live) p[i] = v[i];
+// Chunk c of a row starts at element c * C, moved left where the row's end
+// cuts it (width >= C).
+template <int C>
+__device__ __forceinline__ uint32_t chunk_col(uint32_t c, uint32_t width) {
+    const uint32_t col = c * C;
+    return col + C <= width ? col : width - C;
 }
 
 // n / d for n < 2^31 by a multiplication: with l = ceil(log2 d) and m =
@@ -61,7 +56,6 @@ __device__ __forceinline__ void store_chunk(T *p, ChunkOf<T> v, int live = kChun
 struct FastDiv {
     uint32_t m;
     int shift;
-    FastDiv() = default;
     explicit FastDiv(uint32_t d) {
         int l = 0;
         while ((uint64_t(1) << l) < d) ++l;
@@ -70,6 +64,88 @@ struct FastDiv {
     }
     __device__ __forceinline__ uint32_t div(uint32_t n) const {
         return uint32_t((uint64_t(n) * m) >> shift);
+    }
+};
+
+// The zeroing of rows of any element type. Rows that nothing else writes go in
+// units of `unit_rows` rows, one wave each, which skip the rows they are told
+// to keep; whole ranges go as flat memory when the rows leave no gap.
+constexpr int kZeroRows = 64;            // most rows of a unit
+constexpr int kZeroWaveBytes = 1 << 14;  // about what one wave of a launch zeroes
+
+struct ZeroRows {
+    char *base = nullptr;
+    int64_t ld = 0;          // bytes from row to row
+    int64_t n_rows = 0;
+    uint32_t row_bytes = 0;  // even
+    uint32_t cpr = 0;        // 16-byte chunks per row, the last one maybe cut
+    FastDiv by_cpr{1};
+    int unit_rows = 1;       // a power of two
+
+    ZeroRows() = default;
+    ZeroRows(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes)
+        : base(static_cast<char *>(p)), ld(rows > 1 ? ld_bytes : bytes), n_rows(rows),
+          row_bytes(uint32_t(bytes)), cpr(uint32_t((bytes + 15) / 16)), by_cpr(cpr) {
+        while (unit_rows < kZeroRows && 2 * unit_rows * bytes <= kZeroWaveBytes) unit_rows *= 2;
+    }
+    __host__ __device__ int64_t units() const { return (n_rows + unit_rows - 1) / unit_rows; }
+
+    __device__ __forceinline__ static void chunk(char *p, int64_t left) {
+        if (left >= 16) {
+            using Z = uint16_t __attribute__((ext_vector_type(8), aligned(2)));
+            __builtin_nontemporal_store(Z{}, reinterpret_cast<Z *>(p));
+        } else {
+            for (int b = 0; b < left; b += 2) *reinterpret_cast<uint16_t *>(p + b) = 0;
+        }
+    }
+    // Zeroes the rows of unit u whose bit in `keep` is 0.
+    __device__ __forceinline__ void unit(int64_t u, uint64_t keep) const {
+        const int lane = threadIdx.x & 63;
+        const int64_t r0 = u * unit_rows;
+        const int rows = int(n_rows - r0 < unit_rows ? n_rows - r0 : unit_rows);
+        if (cpr >= 64) {  // a row at a time
+            for (int r = 0; r < rows; ++r) {
+                if ((keep >> r) & 1) continue;
+                char *p = base + (r0 + r) * ld;
+#pragma unroll 4
+                for (uint32_t at = lane * 16; at < row_bytes; at += 1024)
+                    chunk(p + at, int64_t(row_bytes) - at);
+            }
+            return;
+        }
+        for (uint32_t c = lane; c < uint32_t(rows) * cpr; c += 64) {
+            const uint32_t r = by_cpr.div(c), at = (c - r * cpr) * 16;
+            if (!((keep >> r) & 1)) chunk(base + (r0 + r) * ld + at, int64_t(row_bytes) - at);
+        }
+    }
+    // Zeroes all rows of units [lo, hi) by `waves` waves, of which this is
+    // number `wave`.
+    __device__ __forceinline__ void range(int64_t lo, int64_t hi, int64_t wave, int64_t waves) const {
+        if (ld != row_bytes) {
+            for (int64_t u = lo + wave; u < hi; u += waves) unit(u, 0);
+            return;
+        }
+        const int64_t r1 = hi * unit_rows < n_rows ? hi * unit_rows : n_rows;
+        char *p = base + lo * unit_rows * ld;
+        const int64_t bytes = (r1 - lo * unit_rows) * ld;
+        for (int64_t at = wave * 4096 + (threadIdx.x & 63) * 16; at < bytes; at += waves * 4096) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) chunk(p + at + k * 1024, bytes - at - k * 1024);
+        }
+    }
+};
+
+// A share of the zeroing that a launch of another kernel carries: its blocks
+// past its own work zero units [lo, hi).
+struct ZeroShare {
+    ZeroRows rows;
+    int64_t lo = 0, hi = 0;
+    // blocks of `waves` waves for it
+    unsigned blocks(int waves) const {
+        const int64_t bytes = (hi - lo) * rows.unit_rows * int64_t(rows.row_bytes);
+        const int64_t per = int64_t(waves) * kZeroWaveBytes;
+        const int64_t n = (bytes + per - 1) / per;
+        return unsigned(n < (1 << 20) ? n : 1 << 20);
     }
 };
 

@@ -12,6 +12,7 @@
 
 #include "vspmm.h"
 #include "bins.hpp"
+#include "grad.hpp"
 #include "../csrc/launch.hpp"
 #include "rows.hpp"
 
@@ -21,233 +22,229 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kI32Max = 2147483647;
+constexpr uint32_t kManyChunks = 1 << 20;  // k_embed: four chunks a lane from here on
+constexpr int64_t kWidthMax = 1 << 24;  // elements of a row
 
 // ------------------------------------------------------------------ kernels
 
-// out[t] = scale * table[ids[t]], or zeros for an id outside the table. The
-// rows' chunks are one flat list: consecutive lanes take consecutive chunks,
-// whatever the width.
-template <typename T, typename I>
+// f(count, k) for k = 0, 8, .. : eight at a time, then four, two and one.
+template <typename F>
+__device__ __forceinline__ void by_eights(int n, F &&f) {
+    int k = 0;
+    for (; k + 8 <= n; k += 8) f(std::integral_constant<int, 8>{}, k);
+    if (n & 4) f(std::integral_constant<int, 4>{}, k), k += 4;
+    if (n & 2) f(std::integral_constant<int, 2>{}, k), k += 2;
+    if (n & 1) f(std::integral_constant<int, 1>{}, k);
+}
+
+// The chunks of a batch of rows as one flat list: consecutive lanes take
+// consecutive chunks whatever the width, a block 256 * U in a row, a lane U of
+// them, 256 apart.
+struct Chunks {
+    uint32_t n, cpr, width;
+    FastDiv by_cpr;
+};
+
+// out[t] = scale * table[ids[t]], or zeros for an id outside the table.
+template <typename T, typename I, int C, int U>
 __global__ void __launch_bounds__(kThreads)
 k_embed(const T *__restrict__ table, int64_t ld_table, int64_t n_rows, const I *__restrict__ ids,
-        uint32_t n_chunks, int width, uint32_t cpr, FastDiv by_cpr, typename Sum<T>::type scale,
-        T *__restrict__ out, int64_t ld_out) {
+        Chunks ch, typename Sum<T>::type scale, T *__restrict__ out, int64_t ld_out) {
     using A = typename Sum<T>::type;
-    const uint32_t g = blockIdx.x * kThreads + threadIdx.x;
-    if (g >= n_chunks) return;
-    const uint32_t t = by_cpr.div(g), col = (g - t * cpr) * kChunk<T>;
-    const int live = width - int(col);
-    const int64_t id = int64_t(ids[t]);
-    ChunkOf<T> v{};
-    if (id >= 0 && id < n_rows) {
-        v = load_chunk(table + id * ld_table + col, live);
+    const uint32_t g0 = blockIdx.x * (kThreads * U) + threadIdx.x;
+    int64_t id[U];
+    uint32_t col[U], t[U];
 #pragma unroll
-        for (int i = 0; i < kChunk<T>; ++i) v[i] = T(A(v[i]) * scale);
+    for (int u = 0; u < U; ++u) {
+        // lanes past the list take its last chunk again and write nothing
+        const uint32_t g = g0 + u * kThreads < ch.n ? g0 + u * kThreads : ch.n - 1;
+        t[u] = ch.by_cpr.div(g);
+        col[u] = chunk_col<C>(g - t[u] * ch.cpr, ch.width);
+        id[u] = int64_t(ids[t[u]]);
     }
-    store_chunk(out + int64_t(t) * ld_out + col, v, live);
+    Vec<T, C> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        v[u] = Vec<T, C>{};
+        if (id[u] >= 0 && id[u] < n_rows) v[u] = load_vec<C>(table + id[u] * ld_table + col[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool real = id[u] >= 0 && id[u] < n_rows;
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[u][i] = real ? T(A(v[u][i]) * scale) : T(0);
+        if (g0 + u * kThreads < ch.n) store_vec<C>(out + int64_t(t[u]) * ld_out + col[u], v[u]);
+    }
 }
 
-// Every row's first `width` elements = 0.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-k_zero_rows(T *__restrict__ out, int64_t ld, uint32_t n_chunks, int width, uint32_t cpr,
-            FastDiv by_cpr) {
-    const uint32_t g = blockIdx.x * kThreads + threadIdx.x;
-    if (g >= n_chunks) return;
-    const uint32_t t = by_cpr.div(g), col = (g - t * cpr) * kChunk<T>;
-    store_chunk(out + int64_t(t) * ld + col, ChunkOf<T>{}, width - int(col));
-}
-
-// The gradient of the lookup: sums of dout's rows over runs of equal ids in
-// the sorted list of tokens. The list is cut into segments of `seg` places; a
-// group of L lanes walks one segment (64 chunks of the width at a time, the
-// grid's y picks which). A run inside a segment is written to its row of
-// grad; a run cut by a segment's border leaves float partial rows, part[2 s]
-// for a run that came in from the left of segment s and part[2 s + 1] for one
-// that starts in s and goes on, which k_grad_join adds in order.
-template <typename T, typename G, int L, bool ADD>
-__global__ void __launch_bounds__(kThreads)
-k_grad_rows(const uint32_t *__restrict__ keys, const int *__restrict__ order, int n, int seg,
-            uint32_t n_rows, const T *__restrict__ dout, int64_t ld_dout, int width,
-            typename Sum<T>::type scale, G *__restrict__ grad, int64_t ld_grad,
-            typename Sum<T>::type *__restrict__ part, int64_t ld_part) {
-    using A = typename Sum<T>::type;
-    constexpr int C = kChunk<T>;
-    const int lane = threadIdx.x & (L - 1);
-    const int64_t s = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-    const int64_t q0 = s * seg;
-    const int64_t col = (int64_t(blockIdx.y) * L + lane) * C;
-    if (q0 >= n || col >= width) return;
-    const int64_t q1 = q0 + seg < n ? q0 + seg : n;
-    const int live = int(width - col < C ? width - col : C);
-    A acc[C] = {};
-    uint32_t key = keys[q0];
-    bool open_left = q0 > 0 && keys[q0 - 1] == key;
-    auto close = [&](bool open_right) {
-        if (key >= n_rows) return;  // ids outside the table sort last
-        if (open_left || open_right) {
-            A *p = part + (2 * s + (open_left ? 0 : 1)) * ld_part + col;
-#pragma unroll
-            for (int i = 0; i < C; ++i) p[i] = acc[i];
-            return;
-        }
-        G *g = grad + int64_t(key) * ld_grad + col;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (i < live) g[i] = G(ADD ? A(g[i]) + acc[i] * scale : acc[i] * scale);
-    };
-    for (int64_t q = q0; q < q1; ++q) {
-        const uint32_t k = keys[q];
-        if (k != key) {
-            close(false);
-            key = k;
-            open_left = false;
-#pragma unroll
-            for (int i = 0; i < C; ++i) acc[i] = 0;
-        }
-        if (key >= n_rows) break;
-        const ChunkOf<T> v = load_chunk(dout + int64_t(order[q]) * ld_dout + col, live);
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] += A(v[i]);
-    }
-    close(q1 < n && keys[q1] == key);
-}
-
-// The runs that cross segments: the group of the segment a run starts in adds
-// its partial rows, left to right.
-template <typename T, typename G, int L, bool ADD>
-__global__ void __launch_bounds__(kThreads)
-k_grad_join(const uint32_t *__restrict__ keys, int n, int seg, uint32_t n_rows, int width,
-            typename Sum<T>::type scale, G *__restrict__ grad, int64_t ld_grad,
-            const typename Sum<T>::type *__restrict__ part, int64_t ld_part) {
-    using A = typename Sum<T>::type;
-    constexpr int C = kChunk<T>;
-    const int lane = threadIdx.x & (L - 1);
-    const int64_t s = int64_t(blockIdx.x) * (kThreads / L) + threadIdx.x / L;
-    const int64_t q0 = s * seg, q1 = q0 + seg;
-    const int64_t col = (int64_t(blockIdx.y) * L + lane) * C;
-    if (q1 >= n || col >= width) return;
-    const uint32_t key = keys[q1];
-    if (key >= n_rows || keys[q1 - 1] != key) return;         // no run crosses out of s
-    if (q0 > 0 && keys[q0] == key && keys[q0 - 1] == key) return;  // it started further left
-    const int live = int(width - col < C ? width - col : C);
-    A acc[C];
-    const A *p = part + (2 * s + 1) * ld_part + col;
-#pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = p[i];
-    for (int64_t j = s + 1; j * seg < n && keys[j * seg] == key; ++j) {
-        p = part + 2 * j * ld_part + col;
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] += p[i];
-    }
-    G *g = grad + int64_t(key) * ld_grad + col;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-        if (i < live) g[i] = G(ADD ? A(g[i]) + acc[i] * scale : acc[i] * scale);
+// The rows of units [zero.lo, zero.hi) = 0.
+__global__ void __launch_bounds__(kThreads) k_zero(ZeroShare zero) {
+    zero.rows.range(zero.lo, zero.hi, int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64,
+                    int64_t(gridDim.x) * (kThreads / 64));
 }
 
 // rows[position[t, k]] = x[t]; a dropped slot (~p) has row p zeroed. A
 // position past the last row is passed over.
-template <typename T>
+template <typename T, int C>
 __global__ void __launch_bounds__(kThreads)
 k_dispatch(const T *__restrict__ x, int64_t ld_x, const int *__restrict__ position, int top_k,
-           uint32_t n_slots, uint32_t n_chunks, int width, uint32_t cpr, FastDiv by_cpr,
-           T *__restrict__ rows, int64_t ld_rows) {
+           uint32_t n_slots, Chunks ch, T *__restrict__ rows, int64_t ld_rows) {
     const uint32_t g = blockIdx.x * kThreads + threadIdx.x;
-    if (g >= n_chunks) return;
-    const uint32_t t = by_cpr.div(g), col = (g - t * cpr) * kChunk<T>;
-    const int live = width - int(col);
-    const ChunkOf<T> v = load_chunk(x + int64_t(t) * ld_x + col, live);
+    if (g >= ch.n) return;
+    const uint32_t t = ch.by_cpr.div(g), col = chunk_col<C>(g - t * ch.cpr, ch.width);
+    const Vec<T, C> v = load_vec<C>(x + int64_t(t) * ld_x + col);
     const int *pos = position + int64_t(t) * top_k;
-    for (int k = 0; k < top_k; ++k) {
-        const int p = pos[k];
-        const uint32_t row = uint32_t(p >= 0 ? p : ~p);
-        if (row < n_slots)
-            store_chunk(rows + int64_t(row) * ld_rows + col, p >= 0 ? v : ChunkOf<T>{}, live);
-    }
+    auto put = [&](auto count, int k) {
+        constexpr int N = decltype(count)::value;
+        int p[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = pos[k + j];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint32_t row = uint32_t(p[j] >= 0 ? p[j] : ~p[j]);
+            if (row < n_slots)
+                store_vec<C>(rows + int64_t(row) * ld_rows + col, p[j] >= 0 ? v : Vec<T, C>{});
+        }
+    };
+    by_eights(top_k, put);
 }
 
 // out[t] = sum over k of weight[t, k] * rows[position[t, k]] (weight null:
-// ones), k ascending, live slots only; one rounding at the end.
-template <typename T, bool WEIGHTED>
+// ones), k ascending, live slots only; one rounding at the end. Up to eight
+// rows in flight; a dropped slot loads row 0 and leaves the sums.
+template <typename T, int C, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads)
 k_combine(const T *__restrict__ rows, int64_t ld_rows, const int *__restrict__ position,
-          const typename Sum<T>::type *__restrict__ weight, int top_k, uint32_t n_slots,
-          uint32_t n_chunks, int width, uint32_t cpr, FastDiv by_cpr, T *__restrict__ out,
-          int64_t ld_out) {
+          const typename Sum<T>::type *__restrict__ weight, int top_k, uint32_t n_slots, Chunks ch,
+          T *__restrict__ out, int64_t ld_out) {
     using A = typename Sum<T>::type;
-    constexpr int C = kChunk<T>;
     const uint32_t g = blockIdx.x * kThreads + threadIdx.x;
-    if (g >= n_chunks) return;
-    const uint32_t t = by_cpr.div(g), col = (g - t * cpr) * C;
-    const int live = width - int(col);
-    const int64_t slot = int64_t(t) * top_k;
+    if (g >= ch.n) return;
+    const uint32_t t = ch.by_cpr.div(g), col = chunk_col<C>(g - t * ch.cpr, ch.width);
+    const int *pos = position + int64_t(t) * top_k;
     A acc[C] = {};
-    for (int k = 0; k < top_k; ++k) {
-        const uint32_t p = uint32_t(position[slot + k]);
-        if (p >= n_slots) continue;  // dropped
-        const ChunkOf<T> v = load_chunk(rows + int64_t(p) * ld_rows + col, live);
-        const A w = WEIGHTED ? weight[slot + k] : A(1);
+    auto take = [&](auto count, int k) {
+        constexpr int N = decltype(count)::value;
+        uint32_t p[N];
+        A w[N];
+        Vec<T, C> v[N];
 #pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] = WEIGHTED ? fma(w, A(v[i]), acc[i]) : acc[i] + A(v[i]);
+        for (int j = 0; j < N; ++j) p[j] = uint32_t(pos[k + j]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            w[j] = WEIGHTED ? weight[int64_t(t) * top_k + k + j] : A(1);
+            v[j] = load_vec<C>(rows + int64_t(p[j] < n_slots ? p[j] : 0) * ld_rows + col);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (p[j] < n_slots) {
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+                    acc[i] = WEIGHTED ? fma(w[j], A(v[j][i]), acc[i]) : acc[i] + A(v[j][i]);
+            }
+    };
+    by_eights(top_k, take);
+    Vec<T, C> o;
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = T(acc[i]);
+    store_vec<C>(out + int64_t(t) * ld_out + col, o);
+}
+
+// N sums per lane to their totals over the wave's lanes: each step sends the
+// half of the values the partner keeps, so N values take 6 + N - 1 - log2 N
+// exchanges. Value wave_total_of(lane) ends in the lane.
+template <int N, typename A>
+__device__ __forceinline__ A wave_totals(A (&a)[N], int lane) {
+    int m = 32;
+#pragma unroll
+    for (int half = N / 2; half >= 1; half /= 2, m /= 2) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const A send = up ? a[i] : a[i + half];
+            const A keep = up ? a[i + half] : a[i];
+            a[i] = keep + __shfl_xor(send, m);
+        }
     }
-    ChunkOf<T> v;
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = T(acc[i]);
-    store_chunk(out + int64_t(t) * ld_out + col, v, live);
+    for (; m >= 1; m /= 2) a[0] += __shfl_xor(a[0], m);
+    return a[0];
 }
 
 // Gradients of the combine: grad_rows[position[t, k]] = weight[t, k] *
 // dout[t] and grad_weight[t, k] = <dout[t], rows[position[t, k]]>; a dropped
-// slot's row and weight gradient are zero. One block per token; the dots' lane
-// sums are added by a butterfly, then wave by wave: a fixed order.
-template <typename T>
+// slot's row and weight gradient are zero. W waves share a token's width, up to
+// eight of its slots at a time; the dots' lane sums are added over the wave,
+// then wave by wave: a fixed order.
+template <typename T, int C, int W>
 __global__ void __launch_bounds__(kThreads)
 k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict__ rows,
                int64_t ld_rows, const int *__restrict__ position,
                const typename Sum<T>::type *__restrict__ weight, int top_k, uint32_t n_slots,
-               int width, T *__restrict__ grad_rows, int64_t ld_grad_rows,
+               uint32_t n_tokens, uint32_t width, uint32_t cpr, T *__restrict__ grad_rows, int64_t ld_grad_rows,
                typename Sum<T>::type *__restrict__ grad_weight) {
     using A = typename Sum<T>::type;
-    constexpr int C = kChunk<T>;
-    __shared__ A sums[kThreads / 64];
-    const int64_t t = blockIdx.x;
+    constexpr int PER = kThreads / 64 / W;  // tokens per block
+    __shared__ A sums[PER][W][8];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int k = 0; k < top_k; ++k) {
-        const int64_t slot = t * top_k + k;
-        const int p = position[slot];
-        const uint32_t row = uint32_t(p >= 0 ? p : ~p);
-        const bool there = row < n_slots, kept = there && p >= 0;
-        const A w = weight[slot];
-        A dot = 0;
-        if (there) {
-            for (int64_t col = int64_t(threadIdx.x) * C; col < width; col += kThreads * C) {
-                const int live = int(width - col < C ? width - col : C);
-                const ChunkOf<T> d = load_chunk(dout + t * ld_dout + col, live);
-                ChunkOf<T> o{};
-                if (kept) {
-                    const ChunkOf<T> y = load_chunk(rows + int64_t(row) * ld_rows + col, live);
+    const int mine = wave / W, part = wave % W;
+    const uint32_t t = blockIdx.x * PER + mine;
+    const bool real = t < n_tokens;
+    const int64_t slot0 = int64_t(t) * top_k;
+    auto batch = [&](auto count, int k) {
+        constexpr int N = decltype(count)::value;
+        A dot[N] = {};
+        if (real) {
+            uint32_t row[N];
+            bool kept[N];
+            A w[N];
 #pragma unroll
-                    for (int i = 0; i < C; ++i) {
-                        dot = fma(A(d[i]), A(y[i]), dot);
-                        o[i] = T(w * A(d[i]));
+            for (int j = 0; j < N; ++j) {
+                const int p = position[slot0 + k + j];
+                row[j] = uint32_t(p >= 0 ? p : ~p);
+                kept[j] = p >= 0 && row[j] < n_slots;
+                w[j] = weight[slot0 + k + j];
+            }
+            for (uint32_t c = part * 64 + lane; c < cpr; c += 64 * W) {
+                const uint32_t col = chunk_col<C>(c, width);
+                const int moved = int(c * C - col);
+                const Vec<T, C> d = load_vec<C>(dout + int64_t(t) * ld_dout + col);
+                Vec<T, C> y[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    y[j] = load_vec<C>(rows + int64_t(kept[j] ? row[j] : 0) * ld_rows + col);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    Vec<T, C> o{};
+                    if (kept[j]) {
+#pragma unroll
+                        for (int i = 0; i < C; ++i) {
+                            if (i >= moved) dot[j] = fma(A(d[i]), A(y[j][i]), dot[j]);
+                            o[i] = T(w[j] * A(d[i]));
+                        }
                     }
+                    if (row[j] < n_slots)
+                        store_vec<C>(grad_rows + int64_t(row[j]) * ld_grad_rows + col, o);
                 }
-                store_chunk(grad_rows + int64_t(row) * ld_grad_rows + col, o, live);
             }
         }
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) dot += __shfl_xor(dot, m);
-        if (lane == 0) sums[wave] = dot;
+        const A total = wave_totals(dot, lane);
+        constexpr int SPAN = 64 / N;  // lanes that hold one value's total
+        if (W == 1) {
+            if (real && lane % SPAN == 0) grad_weight[slot0 + k + lane / SPAN] = total;
+            return;
+        }
+        if (lane % SPAN == 0) sums[mine][part][lane / SPAN] = total;
         __syncthreads();
-        if (threadIdx.x == 0) {
-            A all = sums[0];
+        if (real && part == 0 && lane < N) {
+            A all = sums[mine][0][lane];
 #pragma unroll
-            for (int w2 = 1; w2 < kThreads / 64; ++w2) all += sums[w2];
-            grad_weight[slot] = all;
+            for (int w2 = 1; w2 < W; ++w2) all += sums[mine][w2][lane];
+            grad_weight[slot0 + k + lane] = all;
         }
         __syncthreads();
-    }
+    };
+    by_eights(top_k, batch);
 }
 
 // --------------------------------------------------------------------- host
@@ -278,17 +275,23 @@ void with_index(int index, F &&f) {
     else f(int32_t{});
 }
 
-// Rows [r0, r0 + count) at a time, so that a launch has fewer than 2^31 chunks.
-template <typename F>
-void by_rows(int64_t n, uint32_t cpr, F &&f) {
-    const int64_t most = std::max<int64_t>(1, (kI32Max - (1 << 20)) / cpr);
-    for (int64_t r0 = 0; r0 < n; r0 += most) f(r0, std::min(most, n - r0));
+// f(chunk size): the 16-byte chunk, or one element for rows shorter than that.
+template <typename T, typename F>
+void with_chunk(int64_t width, F &&f) {
+    if (width >= kChunk<T>) f(std::integral_constant<int, kChunk<T>>{});
+    else f(std::integral_constant<int, 1>{});
 }
-template <typename T>
-uint32_t chunks_of(int64_t width) {
-    return uint32_t((width + kChunk<T> - 1) / kChunk<T>);
+
+// f(r0, chunks) over rows [r0, ..), as many at a time as have fewer than 2^31
+// chunks of C elements.
+template <int C, typename F>
+void by_rows(int64_t n, int64_t width, F &&f) {
+    const uint32_t cpr = uint32_t((width + C - 1) / C);
+    const int64_t most = (kI32Max - (1 << 20)) / cpr;
+    for (int64_t r0 = 0; r0 < n; r0 += most)
+        f(r0, Chunks{uint32_t(std::min(most, n - r0)) * cpr, cpr, uint32_t(width), FastDiv(cpr)});
 }
-unsigned blocks_of(uint32_t n_chunks) { return (n_chunks + kThreads - 1) / kThreads; }
+unsigned blocks_of(uint32_t n, int per) { return (n + per - 1) / per; }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -312,13 +315,31 @@ Passes passes_for(int64_t limit) {
     return {count, (bits + count - 1) / count};
 }
 
-// A segment of the sorted tokens in k_grad_rows.
-int segment_of(int64_t, int64_t) { return 32; }
+// How k_grad_rows cuts the work: lanes per group, slices of the width, places
+// per segment.
+struct GradPlan {
+    int chunk, lanes, slices, seg;
+    int64_t cpr, segs;
+};
+GradPlan grad_plan(int elt, int64_t width, int64_t n) {
+    GradPlan g;
+    g.chunk = width >= 16 / elt_bytes(elt) ? 16 / elt_bytes(elt) : 1;
+    g.cpr = (width + g.chunk - 1) / g.chunk;
+    g.lanes = g.cpr > 16 ? 64 : 16;
+    g.slices = int((g.cpr + g.lanes - 1) / g.lanes);
+    // enough groups for the card's 8,192 waves, as far as segments of 4 go
+    const int most = g.lanes, least = 4;
+    g.seg = least;
+    while (g.seg < most && n * g.slices >= int64_t(2 * g.seg) * 8192) g.seg *= 2;
+    g.segs = (n + g.seg - 1) / g.seg;
+    return g;
+}
 
 struct GradWs {
     uint32_t *keys[2];
     int *pay[2];
     int *counts;
+    int *list, *listed;
     void *part;
     int64_t ld_part;
     size_t bytes;
@@ -332,20 +353,47 @@ GradWs carve_grad(int elt, int64_t n_rows, int64_t width, int64_t n, void *base)
         at += up256(bytes);
         return r;
     };
-    for (int i = 0; i < 2; ++i) w.keys[i] = reinterpret_cast<uint32_t *>(take(size_t(n) * 4));
-    for (int i = 0; i < 2; ++i) w.pay[i] = reinterpret_cast<int *>(take(size_t(n) * 4));
-    w.counts = reinterpret_cast<int *>(take((size_t(4) * bin_blocks(n)) << passes_for(n_rows).bits));
-    const int c = 16 / elt_bytes(elt);
-    w.ld_part = (width + c - 1) / c * c;
-    const int seg = segment_of(n, width);
-    const size_t segs = size_t((n + seg - 1) / seg);
-    w.part = take(2 * segs * size_t(w.ld_part) * (elt == VSPMM_ELT_F64 ? 8 : 4));
+    const GradPlan g = grad_plan(elt, width, n);
+    const bool sorted = n > kRankMax;  // by passes, through a second copy
+    for (int i = 0; i < 2; ++i) {
+        w.keys[i] = reinterpret_cast<uint32_t *>(take(i == 0 || sorted ? size_t(n) * 4 : 0));
+        w.pay[i] = reinterpret_cast<int *>(take(i == 0 || sorted ? size_t(n) * 4 : 0));
+    }
+    w.counts = reinterpret_cast<int *>(
+        take(sorted ? (size_t(4) * bin_blocks(n)) << passes_for(n_rows).bits : 0));
+    w.listed = reinterpret_cast<int *>(take(4));
+    w.list = reinterpret_cast<int *>(take(size_t(g.segs) * 4));
+    w.ld_part = g.cpr * g.chunk;
+    w.part = take(g.segs > 1 ? 2 * size_t(g.segs) * size_t(w.ld_part) * (elt == VSPMM_ELT_F64 ? 8 : 4) : 0);
     w.bytes = at;
     return w;
 }
 
+// Hands out the units of the table's rows that the gradient's launches zero:
+// each takes about as many bytes as its other blocks leave time for, the sums'
+// launch what is left.
+struct ZeroPlan {
+    ZeroRows rows;
+    int64_t next = 0, units = 0;
+    ZeroShare take(int64_t bytes) {
+        ZeroShare z;
+        z.rows = rows;
+        z.lo = next;
+        if (units > 0) {
+            const int64_t unit = int64_t(rows.row_bytes) * rows.unit_rows;
+            next = std::min(units, next + (bytes + unit - 1) / unit);
+        }
+        z.hi = next;
+        return z;
+    }
+};
+constexpr int64_t kMB = 1 << 20;
+constexpr int64_t kZeroRank = 16 * kMB, kZeroCount = 24 * kMB, kZeroPlace = 48 * kMB,
+                  kZeroJoin = 24 * kMB;
+
 vspmm_status check_rows(int64_t n, int64_t width, int64_t ld, const void *p) {
     if (!fits(n) || !fits(width) || ld < 0) return VSPMM_ERR_DIM;
+    if (width > kWidthMax) return VSPMM_ERR_UNSUPPORTED;
     if (n > 0 && width > 0 && !p) return VSPMM_ERR_NULL;
     return VSPMM_OK;
 }
@@ -356,25 +404,52 @@ vspmm_status check_out(int64_t n, int64_t width, int64_t ld, const void *p) {
 }
 
 template <typename T, typename G, bool ADD>
-void launch_grad(const GradWs &w, const uint32_t *keys, const int *order, int64_t n, int seg,
-                 int64_t n_rows, const void *dout, int64_t ld_dout, int64_t width, double scale,
-                 void *grad, int64_t ld_grad, hipStream_t s) {
+void launch_grad(const GradPlan &g, const GradWs &w, const uint32_t *keys, const int *order,
+                 int64_t n, int64_t n_rows, const void *dout, int64_t ld_dout, int64_t width,
+                 double scale, void *grad, int64_t ld_grad, ZeroPlan &zero, hipStream_t s) {
     using A = typename Sum<T>::type;
-    const int64_t segs = (n + seg - 1) / seg;
-    auto go = [&](auto lanes) {
-        constexpr int L = decltype(lanes)::value;
-        const dim3 grid(unsigned((segs + kThreads / L - 1) / (kThreads / L)),
-                        unsigned((chunks_of<T>(width) + L - 1) / L));
-        hipLaunchKernelGGL((k_grad_rows<T, G, L, ADD>), grid, dim3(kThreads), 0, s, keys, order,
-                           int(n), seg, uint32_t(n_rows), static_cast<const T *>(dout), ld_dout,
-                           int(width), A(scale), static_cast<G *>(grad), ld_grad,
-                           static_cast<A *>(w.part), w.ld_part);
-        hipLaunchKernelGGL((k_grad_join<T, G, L, ADD>), grid, dim3(kThreads), 0, s, keys, int(n),
-                           seg, uint32_t(n_rows), int(width), A(scale), static_cast<G *>(grad),
-                           ld_grad, static_cast<const A *>(w.part), w.ld_part);
+    GradArgs<T, G> a;
+    a.keys = keys;
+    a.order = order;
+    a.n = int(n);
+    a.seg = g.seg;
+    a.n_rows = uint32_t(n_rows);
+    a.dout = static_cast<const T *>(dout);
+    a.ld_dout = ld_dout;
+    a.width = int(width);
+    a.cpr = uint32_t(g.cpr);
+    a.slices = uint32_t(g.slices);
+    a.by_slices = FastDiv(uint32_t(g.slices));
+    a.scale = A(scale);
+    a.grad = static_cast<G *>(grad);
+    a.ld_grad = ld_grad;
+    a.part = static_cast<A *>(w.part);
+    a.ld_part = w.ld_part;
+    a.list = w.list;
+    a.listed = w.listed;
+    auto go = [&](auto chunk, auto lanes) {
+        constexpr int C = decltype(chunk)::value, L = decltype(lanes)::value, PER = kGradThreads / L;
+        constexpr int WAVES = kGradThreads / 64;
+        const int64_t items = g.segs * g.slices;
+        const unsigned sum_blocks = unsigned((items + PER - 1) / PER);
+        const bool join = g.segs > 1;
+        const int64_t rest = (zero.units - zero.next) * int64_t(zero.rows.row_bytes) *
+                             zero.rows.unit_rows;
+        const ZeroShare z = zero.take(join ? rest - std::min(rest / 4, kZeroJoin) : rest);
+        hipLaunchKernelGGL((k_grad_rows<T, G, C, L, ADD>), dim3(sum_blocks + z.blocks(WAVES)),
+                           dim3(kGradThreads), 0, s, a, sum_blocks, z);
+        if (!join) return;
+        const ZeroShare zj = zero.take(rest);
+        const unsigned join_blocks = unsigned(std::min<int64_t>(items, 2048));
+        hipLaunchKernelGGL((k_grad_join<T, G, C, L, ADD>),
+                           dim3(join_blocks + zj.blocks(WAVES)), dim3(kGradThreads), 0, s,
+                           a, join_blocks, zj);
     };
-    if (chunks_of<T>(width) > 16) go(std::integral_constant<int, 64>{});
-    else go(std::integral_constant<int, 16>{});
+    const std::integral_constant<int, 64> wide;
+    const std::integral_constant<int, 16> narrow;
+    if (g.chunk == 1) go(std::integral_constant<int, 1>{}, narrow);
+    else if (g.lanes == 64) go(std::integral_constant<int, kChunk<T>>{}, wide);
+    else go(std::integral_constant<int, kChunk<T>>{}, narrow);
 }
 
 }  // namespace
@@ -393,14 +468,20 @@ vspmm_status vspmm_embed(vspmm_elt elt, int64_t n_rows, int64_t width, const voi
         with_index(index, [&](auto i) {
             using T = decltype(e);
             using I = decltype(i);
-            const uint32_t cpr = chunks_of<T>(width);
-            by_rows(n, cpr, [&](int64_t r0, int64_t count) {
-                const uint32_t chunks = uint32_t(count) * cpr;
-                hipLaunchKernelGGL((k_embed<T, I>), dim3(blocks_of(chunks)), dim3(kThreads), 0,
-                                   stream, static_cast<const T *>(table), ld_table, n_rows,
-                                   static_cast<const I *>(ids) + r0, chunks, int(width), cpr,
-                                   FastDiv(cpr), typename Sum<T>::type(scale),
-                                   static_cast<T *>(out) + r0 * ld_out, ld_out);
+            with_chunk<T>(width, [&](auto chunk) {
+                constexpr int C = decltype(chunk)::value;
+                by_rows<C>(n, width, [&](int64_t r0, Chunks ch) {
+                    auto go = [&](auto per) {
+                        constexpr int U = decltype(per)::value;
+                        hipLaunchKernelGGL((k_embed<T, I, C, U>), dim3(blocks_of(ch.n, kThreads * U)),
+                                           dim3(kThreads), 0, stream, static_cast<const T *>(table),
+                                           ld_table, n_rows, static_cast<const I *>(ids) + r0, ch,
+                                           typename Sum<T>::type(scale),
+                                           static_cast<T *>(out) + r0 * ld_out, ld_out);
+                    };
+                    if (ch.n >= kManyChunks) go(std::integral_constant<int, 4>{});
+                    else go(std::integral_constant<int, 1>{});
+                });
             });
         });
     });
@@ -412,6 +493,9 @@ vspmm_status vspmm_embed_grad_workspace_size(vspmm_elt elt, int64_t n_rows, int6
     if (!bytes) return VSPMM_ERR_NULL;
     if (!known_elt(elt)) return VSPMM_ERR_ENUM;
     if (!fits(n_rows) || n_rows == kI32Max || !fits(width) || !fits(n)) return VSPMM_ERR_DIM;
+    if (width > kWidthMax) return VSPMM_ERR_UNSUPPORTED;
+    const GradPlan g = grad_plan(elt, width, n);
+    if (g.segs * g.slices > 1 << 24) return VSPMM_ERR_UNSUPPORTED;
     *bytes = n_rows && width && n ? carve_grad(elt, n_rows, width, n, nullptr).bytes : 0;
     return VSPMM_OK;
 }
@@ -431,48 +515,62 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
     if (need > 0 && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)))
         return VSPMM_ERR_WORKSPACE;
     if (n_rows == 0 || width == 0) return VSPMM_OK;
-    if (!accumulate)
-        with_elt(grad_elt, [&](auto e) {
-            using G = decltype(e);
-            const uint32_t cpr = chunks_of<G>(width);
-            by_rows(n_rows, cpr, [&](int64_t r0, int64_t count) {
-                const uint32_t chunks = uint32_t(count) * cpr;
-                hipLaunchKernelGGL(k_zero_rows<G>, dim3(blocks_of(chunks)), dim3(kThreads), 0,
-                                   stream, static_cast<G *>(grad) + r0 * ld_grad, ld_grad, chunks,
-                                   int(width), cpr, FastDiv(cpr));
-            });
-        });
-    if (n == 0) return launched();
+    ZeroPlan zero;
+    if (!accumulate) {
+        zero.rows = ZeroRows(grad, ld_grad * elt_bytes(grad_elt), n_rows, width * elt_bytes(grad_elt));
+        zero.units = zero.rows.units();
+    }
+    if (n == 0) {
+        if (accumulate) return VSPMM_OK;
+        const ZeroShare z = zero.take(int64_t(1) << 60);
+        hipLaunchKernelGGL(k_zero, dim3(z.blocks(kThreads / 64)), dim3(kThreads), 0, stream,
+                           z);
+        return launched();
+    }
+    const GradPlan plan = grad_plan(elt, width, n);
     const GradWs w = carve_grad(elt, n_rows, width, n, ws);
-    const Passes ps = passes_for(n_rows);
-    const int piece = bin_piece(n), nb = bin_blocks(n), bins = 1 << ps.bits;
-    const size_t lds = bin_lds(bins);
-    const uint32_t *keys = nullptr;
-    const int *order = nullptr;
-    auto pass = [&](auto *src, int k) {
-        using I = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
-        hipLaunchKernelGGL(k_bin_count<I>, dim3(nb), dim3(kBinThreads), size_t(bins) * 4, stream,
-                           src, n, n_rows, k * ps.bits, bins, piece, w.counts);
-        allow_dynamic(reinterpret_cast<const void *>(&k_bin_place<I, PlaceKeys>), lds);
-        const PlaceKeys to{w.keys[k & 1], w.pay[k & 1], order};
-        hipLaunchKernelGGL((k_bin_place<I, PlaceKeys>), dim3(nb), dim3(kBinThreads), lds, stream,
-                           src, n, n_rows, k * ps.bits, bins, ps.bits, piece, w.counts, to,
-                           static_cast<int *>(nullptr));
-        keys = to.keys;
-        order = to.pay;
-    };
-    with_index(index, [&](auto i) { pass(static_cast<const decltype(i) *>(ids), 0); });
-    for (int k = 1; k < ps.count; ++k) pass(keys, k);
-    const int seg = segment_of(n, width);
+    const uint32_t *keys = w.keys[0];
+    const int *order = w.pay[0];
+    with_index(index, [&](auto i) {
+        using I = decltype(i);
+        if (n <= kRankMax) {
+            const ZeroShare z = zero.take(kZeroRank);
+            const int nb = int((n + kRankTile - 1) / kRankTile);
+            hipLaunchKernelGGL(k_rank<I>, dim3(nb + z.blocks(kRankThreads / 64)),
+                               dim3(kRankThreads), 0, stream, static_cast<const I *>(ids), int(n),
+                               n_rows, nb, PlaceKeys{w.keys[0], w.pay[0], nullptr}, w.listed, z);
+            return;
+        }
+        const Passes ps = passes_for(n_rows);
+        const int bins = 1 << ps.bits, piece = bin_piece(n), nb = bin_blocks(n);
+        order = nullptr;
+        auto pass = [&](auto *src, int k) {
+            using S = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
+            const BinPass<S> p{src, n, n_rows, k * ps.bits, bins, piece, nb};
+            ZeroShare z = zero.take(kZeroCount);
+            hipLaunchKernelGGL(k_bin_count<S>, dim3(nb + z.blocks(kBinWaves)),
+                               dim3(kBinThreads), size_t(bins) * 4, stream, p, w.counts, w.listed, z);
+            allow_dynamic(reinterpret_cast<const void *>(&k_bin_place<S, PlaceKeys>), bin_lds(bins));
+            const PlaceKeys to{w.keys[k & 1], w.pay[k & 1], order};
+            z = zero.take(kZeroPlace);
+            hipLaunchKernelGGL((k_bin_place<S, PlaceKeys>), dim3(nb + z.blocks(kBinWaves)),
+                               dim3(kBinThreads), bin_lds(bins), stream, p, ps.bits, w.counts, to,
+                               static_cast<int *>(nullptr), z);
+            keys = to.keys;
+            order = to.pay;
+        };
+        pass(static_cast<const I *>(ids), 0);
+        for (int k = 1; k < ps.count; ++k) pass(keys, k);
+    });
     auto sum = [&](auto e, auto g) {
         using T = decltype(e);
         using G = decltype(g);
         if (accumulate)
-            launch_grad<T, G, true>(w, keys, order, n, seg, n_rows, dout, ld_dout, width, scale,
-                                    grad, ld_grad, stream);
+            launch_grad<T, G, true>(plan, w, keys, order, n, n_rows, dout, ld_dout, width, scale, grad,
+                                    ld_grad, zero, stream);
         else
-            launch_grad<T, G, false>(w, keys, order, n, seg, n_rows, dout, ld_dout, width, scale,
-                                     grad, ld_grad, stream);
+            launch_grad<T, G, false>(plan, w, keys, order, n, n_rows, dout, ld_dout, width, scale, grad,
+                                     ld_grad, zero, stream);
     };
     with_elt(elt, [&](auto e) {
         if (grad_elt == elt) sum(e, e);
@@ -487,7 +585,8 @@ vspmm_status vspmm_route_workspace_size(int64_t n_tokens, int64_t top_k, int64_t
     if (!fits(n_tokens) || !fits(top_k) || !fits(n_experts) || !fits(n_tokens * top_k))
         return VSPMM_ERR_DIM;
     if (n_experts + 1 > kBinMax) return VSPMM_ERR_UNSUPPORTED;
-    *bytes = up256(size_t(4) * bin_blocks(n_tokens * top_k) * size_t(n_experts + 1));
+    const int tiles = bin_blocks(n_tokens * top_k);
+    *bytes = tiles > 1 ? up256(size_t(4) * tiles * size_t(n_experts + 1)) : 0;
     return VSPMM_OK;
 }
 
@@ -503,22 +602,24 @@ vspmm_status vspmm_route(vspmm_index index, int64_t n_tokens, int64_t top_k, int
         return VSPMM_ERR_WORKSPACE;
     const int bins = int(n_experts) + 1;
     if (n == 0) {
-        const uint32_t chunks = chunks_of<int>(bins);
-        hipLaunchKernelGGL(k_zero_rows<int>, dim3(blocks_of(chunks)), dim3(kThreads), 0, stream,
-                           offsets, int64_t(bins), chunks, bins, chunks, FastDiv(chunks));
+        ZeroShare z;
+        z.rows = ZeroRows(offsets, int64_t(bins) * 4, 1, int64_t(bins) * 4);
+        z.hi = 1;
+        hipLaunchKernelGGL(k_zero, dim3(1), dim3(kThreads), 0, stream, z);
         return launched();
     }
     const int piece = bin_piece(n), nb = bin_blocks(n);
-    const size_t lds = bin_lds(bins);
     with_index(index, [&](auto i) {
         using I = decltype(i);
         int *counts = static_cast<int *>(ws);
-        hipLaunchKernelGGL(k_bin_count<I>, dim3(nb), dim3(kBinThreads), size_t(bins) * 4, stream,
-                           static_cast<const I *>(experts), n, n_experts, -1, bins, piece, counts);
-        allow_dynamic(reinterpret_cast<const void *>(&k_bin_place<I, PlaceRoute>), lds);
-        hipLaunchKernelGGL((k_bin_place<I, PlaceRoute>), dim3(nb), dim3(kBinThreads), lds, stream,
-                           static_cast<const I *>(experts), n, n_experts, -1, bins,
-                           bits_of(n_experts), piece, counts, PlaceRoute{order, position}, offsets);
+        const BinPass<I> p{static_cast<const I *>(experts), n, n_experts, -1, bins, piece, nb};
+        if (nb > 1)
+            hipLaunchKernelGGL(k_bin_count<I>, dim3(nb), dim3(kBinThreads), size_t(bins) * 4, stream,
+                               p, counts, static_cast<int *>(nullptr), ZeroShare{});
+        allow_dynamic(reinterpret_cast<const void *>(&k_bin_place<I, PlaceRoute>), bin_lds(bins));
+        hipLaunchKernelGGL((k_bin_place<I, PlaceRoute>), dim3(nb), dim3(kBinThreads), bin_lds(bins),
+                           stream, p, bits_of(n_experts), counts, PlaceRoute{order, position}, offsets,
+                           ZeroShare{});
     });
     return launched();
 }
@@ -535,13 +636,14 @@ vspmm_status vspmm_dispatch(vspmm_elt elt, int64_t n_tokens, int64_t top_k, int6
     if (n == 0 || width == 0) return VSPMM_OK;
     with_elt(elt, [&](auto e) {
         using T = decltype(e);
-        const uint32_t cpr = chunks_of<T>(width);
-        by_rows(n_tokens, cpr, [&](int64_t r0, int64_t count) {
-            const uint32_t chunks = uint32_t(count) * cpr;
-            hipLaunchKernelGGL(k_dispatch<T>, dim3(blocks_of(chunks)), dim3(kThreads), 0, stream,
-                               static_cast<const T *>(x) + r0 * ld_x, ld_x, position + r0 * top_k,
-                               int(top_k), uint32_t(n), chunks, int(width), cpr, FastDiv(cpr),
-                               static_cast<T *>(rows), ld_rows);
+        with_chunk<T>(width, [&](auto chunk) {
+            constexpr int C = decltype(chunk)::value;
+            by_rows<C>(n_tokens, width, [&](int64_t r0, Chunks ch) {
+                hipLaunchKernelGGL((k_dispatch<T, C>), dim3(blocks_of(ch.n, kThreads)), dim3(kThreads),
+                                   0, stream, static_cast<const T *>(x) + r0 * ld_x, ld_x,
+                                   position + r0 * top_k, int(top_k), uint32_t(n), ch,
+                                   static_cast<T *>(rows), ld_rows);
+            });
         });
     });
     return launched();
@@ -560,20 +662,21 @@ vspmm_status vspmm_combine(vspmm_elt elt, int64_t n_tokens, int64_t top_k, int64
     with_elt(elt, [&](auto e) {
         using T = decltype(e);
         using A = typename Sum<T>::type;
-        const uint32_t cpr = chunks_of<T>(width);
-        by_rows(n_tokens, cpr, [&](int64_t r0, int64_t count) {
-            const uint32_t chunks = uint32_t(count) * cpr;
-            auto go = [&](auto weighted) {
-                constexpr bool W = decltype(weighted)::value;
-                hipLaunchKernelGGL((k_combine<T, W>), dim3(blocks_of(chunks)), dim3(kThreads), 0,
-                                   stream, static_cast<const T *>(rows), ld_rows,
-                                   position + r0 * top_k,
-                                   W ? static_cast<const A *>(weight) + r0 * top_k : nullptr,
-                                   int(top_k), uint32_t(n), chunks, int(width), cpr, FastDiv(cpr),
-                                   static_cast<T *>(out) + r0 * ld_out, ld_out);
-            };
-            if (weight) go(std::true_type{});
-            else go(std::false_type{});
+        with_chunk<T>(width, [&](auto chunk) {
+            constexpr int C = decltype(chunk)::value;
+            by_rows<C>(n_tokens, width, [&](int64_t r0, Chunks ch) {
+                auto go = [&](auto weighted) {
+                    constexpr bool W = decltype(weighted)::value;
+                    hipLaunchKernelGGL((k_combine<T, C, W>), dim3(blocks_of(ch.n, kThreads)),
+                                       dim3(kThreads), 0, stream, static_cast<const T *>(rows),
+                                       ld_rows, position + r0 * top_k,
+                                       W ? static_cast<const A *>(weight) + r0 * top_k : nullptr,
+                                       int(top_k), uint32_t(n), ch,
+                                       static_cast<T *>(out) + r0 * ld_out, ld_out);
+                };
+                if (weight) go(std::true_type{});
+                else go(std::false_type{});
+            });
         });
     });
     return launched();
@@ -595,11 +698,29 @@ vspmm_status vspmm_combine_grad(vspmm_elt elt, int64_t n_tokens, int64_t top_k, 
     with_elt(elt, [&](auto e) {
         using T = decltype(e);
         using A = typename Sum<T>::type;
-        hipLaunchKernelGGL(k_combine_grad<T>, dim3(unsigned(n_tokens)), dim3(kThreads), 0, stream,
-                           static_cast<const T *>(dout), ld_dout, static_cast<const T *>(rows),
-                           ld_rows, position, static_cast<const A *>(weight), int(top_k),
-                           uint32_t(n), int(width), static_cast<T *>(grad_rows), ld_grad_rows,
-                           static_cast<A *>(grad_weight));
+        with_chunk<T>(width, [&](auto chunk) {
+            constexpr int C = decltype(chunk)::value;
+            const uint32_t cpr = uint32_t((width + C - 1) / C);
+            auto go = [&](auto waves) {
+                constexpr int W = decltype(waves)::value;
+                const int64_t most = int64_t(1) << 22;  // tokens a launch
+                for (int64_t t0 = 0; t0 < n_tokens; t0 += most) {
+                    const uint32_t count = uint32_t(std::min(most, n_tokens - t0));
+                    const int64_t s0 = t0 * top_k;
+                    hipLaunchKernelGGL((k_combine_grad<T, C, W>),
+                                       dim3(blocks_of(count, kThreads / 64 / W)), dim3(kThreads), 0,
+                                       stream, static_cast<const T *>(dout) + t0 * ld_dout, ld_dout,
+                                       static_cast<const T *>(rows), ld_rows, position + s0,
+                                       static_cast<const A *>(weight) + s0, int(top_k), uint32_t(n),
+                                       count, uint32_t(width), cpr, static_cast<T *>(grad_rows),
+                                       ld_grad_rows, static_cast<A *>(grad_weight) + s0);
+                }
+            };
+            // a wave per 64 chunks of the width, as far as the block's four go
+            if (cpr > 128) go(std::integral_constant<int, 4>{});
+            else if (cpr > 64) go(std::integral_constant<int, 2>{});
+            else go(std::integral_constant<int, 1>{});
+        });
     });
     return launched();
 }
