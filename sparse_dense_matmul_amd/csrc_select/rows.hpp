@@ -42,6 +42,22 @@ __device__ __forceinline__ void store_vec(T *p, Vec<T, C> v) {
     *reinterpret_cast<Vec<T, C> *>(p) = v;
 }
 
+// The same past the caches' replacement order, for streams read or written once.
+template <int C, typename T>
+__device__ __forceinline__ Vec<T, C> load_once(const T *p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const Vec<T, C> *>(p));
+}
+template <int C, typename T>
+__device__ __forceinline__ void store_once(T *p, Vec<T, C> v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<Vec<T, C> *>(p));
+}
+
+template <bool ONCE, int C, typename T>
+__device__ __forceinline__ Vec<T, C> load_as(const T *p) {
+    if constexpr (ONCE) return load_once<C>(p);
+    else return load_vec<C>(p);
+}
+
 // Chunk c of a row starts at element c * C, moved left where the row's end
 // cuts it (width >= C).
 template <int C>
@@ -81,24 +97,28 @@ struct ZeroRows {
     uint32_t cpr = 0;        // 16-byte chunks per row, the last one maybe cut
     FastDiv by_cpr{1};
     int unit_rows = 1;       // a power of two
+    bool once = false;       // nontemporal stores
 
     ZeroRows() = default;
-    ZeroRows(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes)
+    ZeroRows(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, bool nontemporal)
         : base(static_cast<char *>(p)), ld(rows > 1 ? ld_bytes : bytes), n_rows(rows),
-          row_bytes(uint32_t(bytes)), cpr(uint32_t((bytes + 15) / 16)), by_cpr(cpr) {
+          row_bytes(uint32_t(bytes)), cpr(uint32_t((bytes + 15) / 16)), by_cpr(cpr), once(nontemporal) {
         while (unit_rows < kZeroRows && 2 * unit_rows * bytes <= kZeroWaveBytes) unit_rows *= 2;
     }
     __host__ __device__ int64_t units() const { return (n_rows + unit_rows - 1) / unit_rows; }
 
+    template <bool ONCE>
     __device__ __forceinline__ static void chunk(char *p, int64_t left) {
         if (left >= 16) {
             using Z = uint16_t __attribute__((ext_vector_type(8), aligned(2)));
-            __builtin_nontemporal_store(Z{}, reinterpret_cast<Z *>(p));
+            if (ONCE) __builtin_nontemporal_store(Z{}, reinterpret_cast<Z *>(p));
+            else *reinterpret_cast<Z *>(p) = Z{};
         } else {
             for (int b = 0; b < left; b += 2) *reinterpret_cast<uint16_t *>(p + b) = 0;
         }
     }
     // Zeroes the rows of unit u whose bit in `keep` is 0.
+    template <bool ONCE>
     __device__ __forceinline__ void unit(int64_t u, uint64_t keep) const {
         const int lane = threadIdx.x & 63;
         const int64_t r0 = u * unit_rows;
@@ -109,20 +129,21 @@ struct ZeroRows {
                 char *p = base + (r0 + r) * ld;
 #pragma unroll 4
                 for (uint32_t at = lane * 16; at < row_bytes; at += 1024)
-                    chunk(p + at, int64_t(row_bytes) - at);
+                    chunk<ONCE>(p + at, int64_t(row_bytes) - at);
             }
             return;
         }
         for (uint32_t c = lane; c < uint32_t(rows) * cpr; c += 64) {
             const uint32_t r = by_cpr.div(c), at = (c - r * cpr) * 16;
-            if (!((keep >> r) & 1)) chunk(base + (r0 + r) * ld + at, int64_t(row_bytes) - at);
+            if (!((keep >> r) & 1)) chunk<ONCE>(base + (r0 + r) * ld + at, int64_t(row_bytes) - at);
         }
     }
     // Zeroes all rows of units [lo, hi) by `waves` waves, of which this is
     // number `wave`.
+    template <bool ONCE>
     __device__ __forceinline__ void range(int64_t lo, int64_t hi, int64_t wave, int64_t waves) const {
         if (ld != row_bytes) {
-            for (int64_t u = lo + wave; u < hi; u += waves) unit(u, 0);
+            for (int64_t u = lo + wave; u < hi; u += waves) unit<ONCE>(u, 0);
             return;
         }
         const int64_t r1 = hi * unit_rows < n_rows ? hi * unit_rows : n_rows;
@@ -130,8 +151,12 @@ struct ZeroRows {
         const int64_t bytes = (r1 - lo * unit_rows) * ld;
         for (int64_t at = wave * 4096 + (threadIdx.x & 63) * 16; at < bytes; at += waves * 4096) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) chunk(p + at + k * 1024, bytes - at - k * 1024);
+            for (int k = 0; k < 4; ++k) chunk<ONCE>(p + at + k * 1024, bytes - at - k * 1024);
         }
+    }
+    __device__ __forceinline__ void range(int64_t lo, int64_t hi, int64_t wave, int64_t waves) const {
+        if (once) range<true>(lo, hi, wave, waves);
+        else range<false>(lo, hi, wave, waves);
     }
 };
 

@@ -73,7 +73,11 @@ k_embed(const T *__restrict__ table, int64_t ld_table, int64_t n_rows, const I *
         const bool real = id[u] >= 0 && id[u] < n_rows;
 #pragma unroll
         for (int i = 0; i < C; ++i) v[u][i] = real ? T(A(v[u][i]) * scale) : T(0);
-        if (g0 + u * kThreads < ch.n) store_vec<C>(out + int64_t(t[u]) * ld_out + col[u], v[u]);
+        if (g0 + u * kThreads < ch.n) {
+            T *o = out + int64_t(t[u]) * ld_out + col[u];
+            if (U > 1) store_once<C>(o, v[u]);  // 37.2 -> 34.7 us at 16,384 x 4,096 bf16
+            else store_vec<C>(o, v[u]);
+        }
     }
 }
 
@@ -111,8 +115,8 @@ k_dispatch(const T *__restrict__ x, int64_t ld_x, const int *__restrict__ positi
 
 // out[t] = sum over k of weight[t, k] * rows[position[t, k]] (weight null:
 // ones), k ascending, live slots only; one rounding at the end. Up to eight
-// rows in flight; a dropped slot loads row 0 and leaves the sums.
-template <typename T, int C, bool WEIGHTED>
+// rows in flight. ONCE: rows larger than the caches are read nontemporally.
+template <typename T, int C, bool WEIGHTED, bool ONCE>
 __global__ void __launch_bounds__(kThreads)
 k_combine(const T *__restrict__ rows, int64_t ld_rows, const int *__restrict__ position,
           const typename Sum<T>::type *__restrict__ weight, int top_k, uint32_t n_slots, Chunks ch,
@@ -131,10 +135,15 @@ k_combine(const T *__restrict__ rows, int64_t ld_rows, const int *__restrict__ p
 #pragma unroll
         for (int j = 0; j < N; ++j) p[j] = uint32_t(pos[k + j]);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            w[j] = WEIGHTED ? weight[int64_t(t) * top_k + k + j] : A(1);
-            v[j] = load_vec<C>(rows + int64_t(p[j] < n_slots ? p[j] : 0) * ld_rows + col);
-        }
+        for (int j = 0; j < N; ++j) w[j] = WEIGHTED ? weight[int64_t(t) * top_k + k + j] : A(1);
+        // a dropped slot loads the row of the live one before it once more
+        uint32_t from[N], last = 0;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) last = p[j] < n_slots ? p[j] : last;
+#pragma unroll
+        for (int j = 0; j < N; ++j) from[j] = last = p[j] < n_slots ? p[j] : last;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = load_as<ONCE, C>(rows + int64_t(from[j]) * ld_rows + col);
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if (p[j] < n_slots) {
@@ -176,7 +185,7 @@ __device__ __forceinline__ A wave_totals(A (&a)[N], int lane) {
 // slot's row and weight gradient are zero. W waves share a token's width, up to
 // eight of its slots at a time; the dots' lane sums are added over the wave,
 // then wave by wave: a fixed order.
-template <typename T, int C, int W>
+template <typename T, int C, int W, bool ONCE>
 __global__ void __launch_bounds__(kThreads)
 k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict__ rows,
                int64_t ld_rows, const int *__restrict__ position,
@@ -186,7 +195,8 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
     using A = typename Sum<T>::type;
     constexpr int PER = kThreads / 64 / W;  // tokens per block
     __shared__ A sums[PER][W][8];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // so rows are scalar
     const int mine = wave / W, part = wave % W;
     const uint32_t t = blockIdx.x * PER + mine;
     const bool real = t < n_tokens;
@@ -198,21 +208,23 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
             uint32_t row[N];
             bool kept[N];
             A w[N];
+            const T *from[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int p = position[slot0 + k + j];
                 row[j] = uint32_t(p >= 0 ? p : ~p);
                 kept[j] = p >= 0 && row[j] < n_slots;
                 w[j] = weight[slot0 + k + j];
+                from[j] = kept[j] ? rows + int64_t(row[j]) * ld_rows : dout + int64_t(t) * ld_dout;
             }
             for (uint32_t c = part * 64 + lane; c < cpr; c += 64 * W) {
                 const uint32_t col = chunk_col<C>(c, width);
                 const int moved = int(c * C - col);
                 const Vec<T, C> d = load_vec<C>(dout + int64_t(t) * ld_dout + col);
                 Vec<T, C> y[N];
+                // a dropped slot loads dout's chunk once more
 #pragma unroll
-                for (int j = 0; j < N; ++j)
-                    y[j] = load_vec<C>(rows + int64_t(kept[j] ? row[j] : 0) * ld_rows + col);
+                for (int j = 0; j < N; ++j) y[j] = load_as<ONCE, C>(from[j] + col);
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
                     Vec<T, C> o{};
@@ -223,8 +235,11 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
                             o[i] = T(w[j] * A(d[i]));
                         }
                     }
-                    if (row[j] < n_slots)
-                        store_vec<C>(grad_rows + int64_t(row[j]) * ld_grad_rows + col, o);
+                    if (row[j] < n_slots) {
+                        T *to = grad_rows + int64_t(row[j]) * ld_grad_rows + col;
+                        if constexpr (ONCE) store_once<C>(to, o);
+                        else store_vec<C>(to, o);
+                    }
                 }
             }
         }
@@ -292,6 +307,14 @@ void by_rows(int64_t n, int64_t width, F &&f) {
         f(r0, Chunks{uint32_t(std::min(most, n - r0)) * cpr, cpr, uint32_t(width), FastDiv(cpr)});
 }
 unsigned blocks_of(uint32_t n, int per) { return (n + per - 1) / per; }
+
+// Rows that the 256 MB last-level cache cannot hold are read, and the
+// gradient's written, nontemporally: combine at 1.07 GB 235 -> 204 us,
+// combine_grad at 0.54 GB 206 -> 183; at 64 MB combine takes 15.6 us with it and
+// 14.0 without.
+bool streams(int64_t n, int64_t width, int elt) {
+    return n * width * elt_bytes(elt) > (int64_t(256) << 20);
+}
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -517,7 +540,11 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
     if (n_rows == 0 || width == 0) return VSPMM_OK;
     ZeroPlan zero;
     if (!accumulate) {
-        zero.rows = ZeroRows(grad, ld_grad * elt_bytes(grad_elt), n_rows, width * elt_bytes(grad_elt));
+        // nontemporal zeroing beside many rows of dout (16,384 tokens, 131,072
+        // rows of 2,048 bf16: 142 -> 130 us), plain where zeroing is nearly all
+        // there is (2,048 tokens, 64,000 rows of 1,024 f32: 60 -> 49 us)
+        zero.rows = ZeroRows(grad, ld_grad * elt_bytes(grad_elt), n_rows, width * elt_bytes(grad_elt),
+                             8 * n >= n_rows);
         zero.units = zero.rows.units();
     }
     if (n == 0) {
@@ -603,7 +630,7 @@ vspmm_status vspmm_route(vspmm_index index, int64_t n_tokens, int64_t top_k, int
     const int bins = int(n_experts) + 1;
     if (n == 0) {
         ZeroShare z;
-        z.rows = ZeroRows(offsets, int64_t(bins) * 4, 1, int64_t(bins) * 4);
+        z.rows = ZeroRows(offsets, int64_t(bins) * 4, 1, int64_t(bins) * 4, false);
         z.hi = 1;
         hipLaunchKernelGGL(k_zero, dim3(1), dim3(kThreads), 0, stream, z);
         return launched();
@@ -665,17 +692,21 @@ vspmm_status vspmm_combine(vspmm_elt elt, int64_t n_tokens, int64_t top_k, int64
         with_chunk<T>(width, [&](auto chunk) {
             constexpr int C = decltype(chunk)::value;
             by_rows<C>(n_tokens, width, [&](int64_t r0, Chunks ch) {
-                auto go = [&](auto weighted) {
-                    constexpr bool W = decltype(weighted)::value;
-                    hipLaunchKernelGGL((k_combine<T, C, W>), dim3(blocks_of(ch.n, kThreads)),
+                auto go = [&](auto weighted, auto once) {
+                    constexpr bool W = decltype(weighted)::value, ONCE = decltype(once)::value;
+                    hipLaunchKernelGGL((k_combine<T, C, W, ONCE>), dim3(blocks_of(ch.n, kThreads)),
                                        dim3(kThreads), 0, stream, static_cast<const T *>(rows),
                                        ld_rows, position + r0 * top_k,
                                        W ? static_cast<const A *>(weight) + r0 * top_k : nullptr,
                                        int(top_k), uint32_t(n), ch,
                                        static_cast<T *>(out) + r0 * ld_out, ld_out);
                 };
-                if (weight) go(std::true_type{});
-                else go(std::false_type{});
+                auto pick = [&](auto once) {
+                    if (weight) go(std::true_type{}, once);
+                    else go(std::false_type{}, once);
+                };
+                if (streams(n, width, elt)) pick(std::true_type{});
+                else pick(std::false_type{});
             });
         });
     });
@@ -701,13 +732,14 @@ vspmm_status vspmm_combine_grad(vspmm_elt elt, int64_t n_tokens, int64_t top_k, 
         with_chunk<T>(width, [&](auto chunk) {
             constexpr int C = decltype(chunk)::value;
             const uint32_t cpr = uint32_t((width + C - 1) / C);
-            auto go = [&](auto waves) {
+            auto go = [&](auto waves, auto once) {
                 constexpr int W = decltype(waves)::value;
+                constexpr bool ONCE = decltype(once)::value;
                 const int64_t most = int64_t(1) << 22;  // tokens a launch
                 for (int64_t t0 = 0; t0 < n_tokens; t0 += most) {
                     const uint32_t count = uint32_t(std::min(most, n_tokens - t0));
                     const int64_t s0 = t0 * top_k;
-                    hipLaunchKernelGGL((k_combine_grad<T, C, W>),
+                    hipLaunchKernelGGL((k_combine_grad<T, C, W, ONCE>),
                                        dim3(blocks_of(count, kThreads / 64 / W)), dim3(kThreads), 0,
                                        stream, static_cast<const T *>(dout) + t0 * ld_dout, ld_dout,
                                        static_cast<const T *>(rows), ld_rows, position + s0,
@@ -717,9 +749,13 @@ vspmm_status vspmm_combine_grad(vspmm_elt elt, int64_t n_tokens, int64_t top_k, 
                 }
             };
             // a wave per 64 chunks of the width, as far as the block's four go
-            if (cpr > 128) go(std::integral_constant<int, 4>{});
-            else if (cpr > 64) go(std::integral_constant<int, 2>{});
-            else go(std::integral_constant<int, 1>{});
+            auto pick = [&](auto once) {
+                if (cpr > 128) go(std::integral_constant<int, 4>{}, once);
+                else if (cpr > 64) go(std::integral_constant<int, 2>{}, once);
+                else go(std::integral_constant<int, 1>{}, once);
+            };
+            if (streams(n, width, elt)) pick(std::true_type{});
+            else pick(std::false_type{});
         });
     });
     return launched();
