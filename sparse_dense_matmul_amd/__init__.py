@@ -124,7 +124,8 @@ class _Lib:
     def __getattr__(self, name):
         if _Lib._handle is None:
             _Lib._handle = _load()
-        return getattr(_Lib._handle, name)
+        fn = self.__dict__[name] = getattr(_Lib._handle, name)  # found directly from now on
+        return fn
 
 
 lib = _Lib()

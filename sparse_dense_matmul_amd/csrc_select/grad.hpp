@@ -4,10 +4,11 @@
 //
 // The list is cut into segments of `seg` places. A group of L lanes walks one
 // segment for L chunks of the width (a slice), eight rows in flight. A run
-// inside a segment goes to its row of grad; a run cut by a segment's border
-// leaves partial rows of the sums' type, part[2 s] for a run that came into
-// segment s from the left and part[2 s + 1] for one that starts in s and goes
-// on, and s is listed for k_grad_join, which adds a listed run's partial rows:
+// inside a segment goes to its row of grad, and so does one that crosses a
+// single border, summed whole in the segment it starts in. A run over two
+// borders or more leaves partial rows of the sums' type, part[2 s + 1] in the
+// segment s it starts in and part[2 s] in those it comes into from the left, and
+// the former is listed for k_grad_join, which adds a listed run's partial rows:
 // L-lane groups a contiguous share each, the shares in order. Segments, shares
 // and so the order of every sum depend only on the ids and sizes.
 #pragma once
@@ -20,6 +21,7 @@
 namespace vspmm {
 
 constexpr int kGradThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kGradRows = 8;  // rows in flight per group
 
 // C sums to a row of the gradient. Of a chunk moved left by `moved` elements,
@@ -44,30 +46,30 @@ __device__ __forceinline__ void write_grad(G *g, const A *acc, A scale, uint32_t
     store_vec<C>(g, o);
 }
 
-template <int C, typename A>
-__device__ __forceinline__ void write_part(A *p, const A *acc) {
-    Vec<A, C> o;
+// A group's C sums per lane as 16-byte pieces, all lanes' first pieces, then
+// their second ones: every access of the group is contiguous.
+template <int C, int L, typename A>
+__device__ __forceinline__ void write_part(A *group, int lane, const A *acc) {
+    constexpr int P = C * sizeof(A) < 16 ? C : int(16 / sizeof(A));
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = acc[i];
-    store_vec<C>(p, o);
-}
-
-// The first place in [lo, n) whose key is above `key` (keys ascending), by all
-// lanes of the wave: each round probes 64 places.
-__device__ __forceinline__ int wave_upper_bound(const uint32_t *keys, int lo, int n, uint32_t key) {
-    const int lane = threadIdx.x & 63;
-    int hi = n;  // the answer lies in [lo, hi]
-    while (lo < hi) {
-        const int step = (hi - lo + 63) / 64;
-        const int64_t at = int64_t(lo) + int64_t(lane) * step;
-        const uint64_t over = __ballot(at >= hi || keys[at < hi ? at : lo] > key);
-        const int f = over ? __ffsll((unsigned long long)over) - 1 : 64;  // first probe above
-        if (f == 0) return lo;
-        const int64_t top = int64_t(lo) + int64_t(f) * step;
-        lo += (f - 1) * step + 1;
-        if (f < 64 && top < hi) hi = int(top);
+    for (int k = 0; k < C / P; ++k) {
+        Vec<A, P> o;
+#pragma unroll
+        for (int i = 0; i < P; ++i) o[i] = acc[k * P + i];
+        store_vec<P>(group + (k * L + lane) * P, o);
     }
-    return lo;
+}
+template <int C, int L, typename A>
+__device__ __forceinline__ Vec<A, C> read_part(const A *group, int lane) {
+    constexpr int P = C * sizeof(A) < 16 ? C : int(16 / sizeof(A));
+    Vec<A, C> v;
+#pragma unroll
+    for (int k = 0; k < C / P; ++k) {
+        const Vec<A, P> o = load_vec<P>(group + (k * L + lane) * P);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[k * P + i] = o[i];
+    }
+    return v;
 }
 
 // What the sums need of the sorted list and the arrays.
@@ -75,7 +77,7 @@ template <typename T, typename G>
 struct GradArgs {
     const uint32_t *keys;
     const int *order;
-    int n, seg;
+    int n, seg, segs;
     uint32_t n_rows;
     const T *dout;
     int64_t ld_dout;
@@ -90,77 +92,71 @@ struct GradArgs {
     int *list, *listed;  // segments whose last run goes on; how many
 };
 
-// Zeroes the rows of units [zero.lo, zero.hi) that no token selects, by the
-// launch's blocks from `first` on.
-template <bool ONCE>
-__device__ __forceinline__ void zero_unselected(const ZeroShare &zero, unsigned first,
-                                                const uint32_t *keys, int n) {
-    const int64_t waves = int64_t(gridDim.x - first) * (kGradThreads / 64);
-    for (int64_t u = zero.lo + int64_t(blockIdx.x - first) * (kGradThreads / 64) + threadIdx.x / 64;
-         u < zero.hi; u += waves) {
-        // is row r selected: the first key at or above r, by binary search
-        const uint32_t r = uint32_t(u * zero.rows.unit_rows) + (threadIdx.x & 63);
-        int lo = 0, hi = n;
-        while (lo < hi) {
-            const int mid = int((unsigned(lo) + unsigned(hi)) / 2);
-            if (keys[mid] < r) lo = mid + 1;
-            else hi = mid;
-        }
-        const bool there = lo < n && keys[lo] == r;
-        zero.rows.unit<ONCE>(u, __ballot(there));
-    }
-}
-
-// Blocks past `sum_blocks` zero their share of rows.
 template <typename T, typename G, int C, int L, bool ADD>
-__global__ void __launch_bounds__(kGradThreads)
-k_grad_rows(GradArgs<T, G> a, unsigned sum_blocks, ZeroShare zero) {
+__global__ void __launch_bounds__(kGradThreads) k_grad_rows(GradArgs<T, G> a) {
     using A = typename Sum<T>::type;
-    if (!ADD && blockIdx.x >= sum_blocks) {
-        if (zero.rows.once) zero_unselected<true>(zero, sum_blocks, a.keys, a.n);
-        else zero_unselected<false>(zero, sum_blocks, a.keys, a.n);
-        return;
-    }
     const int lane = threadIdx.x & (L - 1);
     const uint32_t unit = blockIdx.x * (kGradThreads / L) + threadIdx.x / L;
     const uint32_t s = a.by_slices.div(unit), slice = unit - s * a.slices;
     const int64_t q0 = int64_t(s) * a.seg;
     if (q0 >= a.n) return;  // a whole group
     const int cnt = int(a.n - q0 < a.seg ? a.n - q0 : a.seg);
+    auto key_at = [&](int64_t q) { return q >= 0 && q < a.n ? a.keys[q] : ~0u; };
+    // this segment's places and the next one's, a lane each, and the keys around
+    const int64_t q1 = q0 + a.seg;
     const uint32_t mine = lane < cnt ? a.keys[q0 + lane] : ~0u;
     const int token = lane < cnt ? a.order[q0 + lane] : 0;
-    const uint32_t left = q0 > 0 ? a.keys[q0 - 1] : ~0u;
-    const uint32_t right = q0 + cnt < a.n ? a.keys[q0 + cnt] : ~0u;
+    const bool in_next = lane < a.seg && q1 + lane < a.n;
+    const uint32_t next = in_next ? a.keys[q1 + lane] : ~0u;
+    const int next_token = in_next ? a.order[q1 + lane] : 0;
+    const uint32_t left = key_at(q0 - 1), left2 = key_at(q0 - a.seg - 1), right2 = key_at(q1 + a.seg);
     auto of = [&](auto x, int j) {
         if constexpr (L == 64) return decltype(x)(__builtin_amdgcn_readlane(int(x), j));
         else return decltype(x)(__shfl(int(x), j, L));
     };
-    // bits of this group: places where a run starts, and live places
+    // of this group's lanes: places where a run starts, live places
     const int shift = L == 64 ? 0 : (threadIdx.x & 63) & ~(L - 1);
     constexpr uint64_t group = L == 64 ? ~0ull : (1ull << (L & 63)) - 1;
+    auto vote = [&](bool x) { return (__ballot(x) >> shift) & group; };
     const uint32_t before = uint32_t(__shfl_up(int(mine), 1, L));
-    const uint64_t starts = (__ballot(lane > 0 && mine != before) >> shift) & group;
-    const int live_places = __popcll((__ballot(mine < a.n_rows) >> shift) & group);
+    const uint64_t starts = vote(lane > 0 && lane < cnt && mine != before);
+    const int live_places = __popcll(vote(mine < a.n_rows));
     if (live_places == 0) return;
+    // the first run: cut by the left border, and all the left segment's if it
+    // starts there and ends here
+    const uint32_t right = of(next, 0);
+    const uint32_t first = of(mine, 0), last = of(mine, live_places - 1);
+    bool open_left = left == first;
+    int q = 0;
+    if (open_left && left2 != first && right != first) {
+        q = starts ? __ffsll((unsigned long long)starts) - 1 : cnt;
+        open_left = false;
+        if (q >= live_places) return;
+    }
+    // the last run: cut by the right border, and this segment's if it starts
+    // here and ends in the next
+    const bool open_right = live_places == cnt && right == last;
+    const bool taken = open_right && (starts != 0 || !open_left) && right2 != last;
+    const int more = taken ? __popcll(vote(next == last)) : 0;
 
     // lanes past the width load the last chunk again and write nothing
     const uint32_t c = slice * L + lane;
     const uint32_t col = chunk_col<C>(c < a.cpr ? c : a.cpr - 1, a.width);
     const T *x = a.dout + col;
     A acc[C] = {};
-    bool open_left = left == of(mine, 0);
-    auto close = [&](uint32_t key, bool open_right) {
-        if (open_left || open_right) {
-            if (c < a.cpr)
-                write_part<C>(a.part + (2 * int64_t(s) + (open_left ? 0 : 1)) * a.ld_part + c * C, acc);
+    auto close = [&](uint32_t key, bool cut) {
+        if (open_left || cut) {
+            write_part<C, L>(a.part + (2 * int64_t(s) + (open_left ? 0 : 1)) * a.ld_part +
+                                 int64_t(slice) * L * C, lane, acc);
             if (!open_left && slice == 0 && lane == 0) a.list[atomicAdd(a.listed, 1)] = int(s);
         } else if (c < a.cpr) {
             write_grad<G, C, ADD>(a.grad + int64_t(key) * a.ld_grad + col, acc, a.scale, c * C - col);
         }
     };
-    auto add = [&](int q, Vec<T, C> v) {
-        if ((starts >> q) & 1) {
-            close(of(mine, q - 1), false);
+    const int begin = q;
+    auto add = [&](int at, Vec<T, C> v) {  // place `at`, or past cnt one of the next segment's
+        if (at > begin && at < cnt && ((starts >> at) & 1)) {
+            close(of(mine, at - 1), false);
             open_left = false;
 #pragma unroll
             for (int i = 0; i < C; ++i) acc[i] = 0;
@@ -168,64 +164,68 @@ k_grad_rows(GradArgs<T, G> a, unsigned sum_blocks, ZeroShare zero) {
 #pragma unroll
         for (int i = 0; i < C; ++i) acc[i] += A(v[i]);
     };
+    auto row = [&](int at) {
+        const int t = at < cnt ? of(token, at) : of(next_token, at - cnt);
+        return load_once<C>(x + int64_t(t) * a.ld_dout);
+    };
     // dout's rows are read once: nontemporal, 345 -> 317 us for 65,536 tokens of
     // 4,096 bf16, 95 -> 80 for 16,384 of 2,048, never slower
-    int q = 0;
-    for (; q + kGradRows <= live_places; q += kGradRows) {
+    const int end = live_places + more;  // more > 0 only behind cnt live places
+    for (; q + kGradRows <= end; q += kGradRows) {
         Vec<T, C> v[kGradRows];
 #pragma unroll
-        for (int u = 0; u < kGradRows; ++u)
-            v[u] = load_once<C>(x + int64_t(of(token, q + u)) * a.ld_dout);
+        for (int u = 0; u < kGradRows; ++u) v[u] = row(q + u);
 #pragma unroll
         for (int u = 0; u < kGradRows; ++u) add(q + u, v[u]);
     }
-    if (q < live_places) {
+    if (q < end) {
         Vec<T, C> v[kGradRows];
 #pragma unroll
         for (int u = 0; u < kGradRows - 1; ++u)
-            if (q + u < live_places) v[u] = load_once<C>(x + int64_t(of(token, q + u)) * a.ld_dout);
+            if (q + u < end) v[u] = row(q + u);
 #pragma unroll
         for (int u = 0; u < kGradRows - 1; ++u)
-            if (q + u < live_places) add(q + u, v[u]);
+            if (q + u < end) add(q + u, v[u]);
     }
-    const uint32_t last = of(mine, live_places - 1);
-    close(last, live_places == cnt && right == last);
+    close(last, open_right && !taken);
 }
 
-// Blocks past `join_blocks` zero their share of rows.
 template <typename T, typename G, int C, int L, bool ADD>
-__global__ void __launch_bounds__(kGradThreads)
-k_grad_join(GradArgs<T, G> a, unsigned join_blocks, ZeroShare zero) {
+__global__ void __launch_bounds__(kJoinThreads) k_grad_join(GradArgs<T, G> a) {
     using A = typename Sum<T>::type;
-    if (!ADD && blockIdx.x >= join_blocks) {
-        if (zero.rows.once) zero_unselected<true>(zero, join_blocks, a.keys, a.n);
-        else zero_unselected<false>(zero, join_blocks, a.keys, a.n);
-        return;
-    }
-    constexpr int GROUPS = kGradThreads / L;
-    __shared__ __align__(16) A sums[kGradThreads * C];
+    constexpr int GROUPS = kJoinThreads / L;
+    __shared__ __align__(16) A sums[kJoinThreads * C];
     const int lane = threadIdx.x & (L - 1), group = threadIdx.x / L;
-    const int64_t items = int64_t(*a.listed) * a.slices;
-    for (int64_t it = blockIdx.x; it < items; it += join_blocks) {
-        const int s = a.list[it / a.slices];
-        const uint32_t slice = uint32_t(it % a.slices);
-        const int q1 = (s + 1) * a.seg;  // <= n: the run goes on past it
-        const uint32_t key = a.keys[q1];
-        const int end = wave_upper_bound(a.keys, q1, a.n, key);
-        // partial rows: the tail of s, then the heads of s + 1 .. last
-        const int parts = (end - 1) / a.seg - s + 1;
+    const int listed = *a.listed;
+    for (int64_t it = blockIdx.x; it < int64_t(a.segs) * a.slices; it += gridDim.x) {
+        const int64_t e = it / a.slices;
+        const uint32_t slice = uint32_t(it - e * a.slices);
+        const int s = a.list[e];  // loaded beside `listed`: used below it alone
+        if (e >= listed) return;
+        // partial rows: the tail of s, then the heads of the segments whose first
+        // key is still the run's; 64 borders at a time
+        uint32_t key = 0;
+        int parts = 1;
+        for (int j = s + 1;; j += 64) {
+            const int64_t at = (int64_t(j) + (threadIdx.x & 63)) * a.seg;
+            const uint32_t k = at < a.n ? a.keys[at] : ~0u;
+            if (j == s + 1) key = __builtin_amdgcn_readlane(k, 0);
+            const uint64_t other = __ballot(k != key);
+            parts += other ? __ffsll((unsigned long long)other) - 1 : 64;
+            if (other) break;
+        }
         const int per = (parts + GROUPS - 1) / GROUPS;
         const int p0 = group * per, p1 = p0 + per < parts ? p0 + per : parts;
         const uint32_t c = slice * L + lane;
-        const uint32_t cc = c < a.cpr ? c : a.cpr - 1;
         A acc[C] = {};
         for (int p = p0; p < p1; p += kGradRows) {
             Vec<A, C> v[kGradRows];
 #pragma unroll
             for (int u = 0; u < kGradRows; ++u)
                 if (p + u < p1)
-                    v[u] = load_vec<C>(
-                        a.part + (2 * int64_t(s + p + u) + (p + u == 0 ? 1 : 0)) * a.ld_part + cc * C);
+                    v[u] = read_part<C, L>(a.part +
+                                               (2 * int64_t(s + p + u) + (p + u == 0 ? 1 : 0)) * a.ld_part +
+                                               int64_t(slice) * L * C, lane);
 #pragma unroll
             for (int u = 0; u < kGradRows; ++u)
                 if (p + u < p1) {
@@ -233,12 +233,12 @@ k_grad_join(GradArgs<T, G> a, unsigned join_blocks, ZeroShare zero) {
                     for (int i = 0; i < C; ++i) acc[i] += v[u][i];
                 }
         }
-        write_part<C>(sums + threadIdx.x * C, acc);
+        write_part<C, L>(sums + group * L * C, lane, acc);
         __syncthreads();
         if (group == 0 && c < a.cpr) {
 #pragma unroll
             for (int g = 1; g < GROUPS; ++g) {
-                const Vec<A, C> v = load_vec<C>(sums + (g * L + lane) * C);
+                const Vec<A, C> v = read_part<C, L>(sums + g * L * C, lane);
 #pragma unroll
                 for (int i = 0; i < C; ++i) acc[i] += v[i];
             }

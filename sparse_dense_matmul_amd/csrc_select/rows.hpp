@@ -83,94 +83,56 @@ struct FastDiv {
     }
 };
 
-// The zeroing of rows of any element type. Rows that nothing else writes go in
-// units of `unit_rows` rows, one wave each, which skip the rows they are told
-// to keep; whole ranges go as flat memory when the rows leave no gap.
-constexpr int kZeroRows = 64;            // most rows of a unit
-constexpr int kZeroWaveBytes = 1 << 14;  // about what one wave of a launch zeroes
-
+// Rows of any element type to zero, by the blocks of a launch past its own
+// `first` ones: one 16-byte store a thread, consecutive threads consecutive
+// chunks. 1.07 GB take 159 us so (6.8 TB/s), 181 with four stores a thread, 186
+// with sixteen: the fewer bytes a wave holds, the narrower the window of
+// addresses being written at a time.
 struct ZeroRows {
     char *base = nullptr;
     int64_t ld = 0;          // bytes from row to row
-    int64_t n_rows = 0;
-    uint32_t row_bytes = 0;  // even
-    uint32_t cpr = 0;        // 16-byte chunks per row, the last one maybe cut
+    int64_t chunks = 0;      // 16-byte chunks of all rows, a row's last one maybe cut;
+                             // of all bytes when no gap is left between rows
+    int64_t bytes = 0;       // of a row, or of all rows; even
+    uint32_t cpr = 0;        // chunks per row, 0 for no gaps
     FastDiv by_cpr{1};
-    int unit_rows = 1;       // a power of two
-    bool once = false;       // nontemporal stores
 
     ZeroRows() = default;
-    ZeroRows(void *p, int64_t ld_bytes, int64_t rows, int64_t bytes, bool nontemporal)
-        : base(static_cast<char *>(p)), ld(rows > 1 ? ld_bytes : bytes), n_rows(rows),
-          row_bytes(uint32_t(bytes)), cpr(uint32_t((bytes + 15) / 16)), by_cpr(cpr), once(nontemporal) {
-        while (unit_rows < kZeroRows && 2 * unit_rows * bytes <= kZeroWaveBytes) unit_rows *= 2;
-    }
-    __host__ __device__ int64_t units() const { return (n_rows + unit_rows - 1) / unit_rows; }
-
-    template <bool ONCE>
-    __device__ __forceinline__ static void chunk(char *p, int64_t left) {
-        if (left >= 16) {
-            using Z = uint16_t __attribute__((ext_vector_type(8), aligned(2)));
-            if (ONCE) __builtin_nontemporal_store(Z{}, reinterpret_cast<Z *>(p));
-            else *reinterpret_cast<Z *>(p) = Z{};
+    ZeroRows(void *p, int64_t ld_bytes, int64_t rows, int64_t row_bytes)
+        : base(static_cast<char *>(p)), ld(ld_bytes) {
+        if (rows <= 1 || ld_bytes == row_bytes) {
+            bytes = rows * row_bytes;
+            chunks = (bytes + 15) / 16;
         } else {
-            for (int b = 0; b < left; b += 2) *reinterpret_cast<uint16_t *>(p + b) = 0;
+            bytes = row_bytes;
+            cpr = uint32_t((row_bytes + 15) / 16);
+            by_cpr = FastDiv(cpr);
+            chunks = rows * cpr;
         }
     }
-    // Zeroes the rows of unit u whose bit in `keep` is 0.
-    template <bool ONCE>
-    __device__ __forceinline__ void unit(int64_t u, uint64_t keep) const {
-        const int lane = threadIdx.x & 63;
-        const int64_t r0 = u * unit_rows;
-        const int rows = int(n_rows - r0 < unit_rows ? n_rows - r0 : unit_rows);
-        if (cpr >= 64) {  // a row at a time
-            for (int r = 0; r < rows; ++r) {
-                if ((keep >> r) & 1) continue;
-                char *p = base + (r0 + r) * ld;
-#pragma unroll 4
-                for (uint32_t at = lane * 16; at < row_bytes; at += 1024)
-                    chunk<ONCE>(p + at, int64_t(row_bytes) - at);
+    // blocks of `threads` threads for it
+    unsigned blocks(int threads) const {
+        const int64_t n = (chunks + threads - 1) / threads;
+        return unsigned(n < (1 << 21) ? n : 1 << 21);
+    }
+    __device__ __forceinline__ void run(unsigned first) const {
+        const int64_t threads = int64_t(gridDim.x - first) * blockDim.x;
+        for (int64_t c = int64_t(blockIdx.x - first) * blockDim.x + threadIdx.x; c < chunks;
+             c += threads) {
+            int64_t row = 0, chunk = c;
+            if (cpr) {
+                row = c < (int64_t(1) << 31) ? by_cpr.div(uint32_t(c)) : c / cpr;
+                chunk = c - row * cpr;
             }
-            return;
+            char *p = base + row * ld + chunk * 16;
+            const int64_t left = bytes - chunk * 16;
+            if (left >= 16) {
+                using Z = uint16_t __attribute__((ext_vector_type(8), aligned(2)));
+                *reinterpret_cast<Z *>(p) = Z{};
+            } else {
+                for (int b = 0; b < left; b += 2) *reinterpret_cast<uint16_t *>(p + b) = 0;
+            }
         }
-        for (uint32_t c = lane; c < uint32_t(rows) * cpr; c += 64) {
-            const uint32_t r = by_cpr.div(c), at = (c - r * cpr) * 16;
-            if (!((keep >> r) & 1)) chunk<ONCE>(base + (r0 + r) * ld + at, int64_t(row_bytes) - at);
-        }
-    }
-    // Zeroes all rows of units [lo, hi) by `waves` waves, of which this is
-    // number `wave`.
-    template <bool ONCE>
-    __device__ __forceinline__ void range(int64_t lo, int64_t hi, int64_t wave, int64_t waves) const {
-        if (ld != row_bytes) {
-            for (int64_t u = lo + wave; u < hi; u += waves) unit<ONCE>(u, 0);
-            return;
-        }
-        const int64_t r1 = hi * unit_rows < n_rows ? hi * unit_rows : n_rows;
-        char *p = base + lo * unit_rows * ld;
-        const int64_t bytes = (r1 - lo * unit_rows) * ld;
-        for (int64_t at = wave * 4096 + (threadIdx.x & 63) * 16; at < bytes; at += waves * 4096) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) chunk<ONCE>(p + at + k * 1024, bytes - at - k * 1024);
-        }
-    }
-    __device__ __forceinline__ void range(int64_t lo, int64_t hi, int64_t wave, int64_t waves) const {
-        if (once) range<true>(lo, hi, wave, waves);
-        else range<false>(lo, hi, wave, waves);
-    }
-};
-
-// A share of the zeroing that a launch of another kernel carries: its blocks
-// past its own work zero units [lo, hi).
-struct ZeroShare {
-    ZeroRows rows;
-    int64_t lo = 0, hi = 0;
-    // blocks of `waves` waves for it
-    unsigned blocks(int waves) const {
-        const int64_t bytes = (hi - lo) * rows.unit_rows * int64_t(rows.row_bytes);
-        const int64_t per = int64_t(waves) * kZeroWaveBytes;
-        const int64_t n = (bytes + per - 1) / per;
-        return unsigned(n < (1 << 20) ? n : 1 << 20);
     }
 };
 

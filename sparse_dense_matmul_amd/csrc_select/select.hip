@@ -81,11 +81,7 @@ k_embed(const T *__restrict__ table, int64_t ld_table, int64_t n_rows, const I *
     }
 }
 
-// The rows of units [zero.lo, zero.hi) = 0.
-__global__ void __launch_bounds__(kThreads) k_zero(ZeroShare zero) {
-    zero.rows.range(zero.lo, zero.hi, int64_t(blockIdx.x) * (kThreads / 64) + threadIdx.x / 64,
-                    int64_t(gridDim.x) * (kThreads / 64));
-}
+__global__ void __launch_bounds__(kThreads) k_zero(ZeroRows zero) { zero.run(0); }
 
 // rows[position[t, k]] = x[t]; a dropped slot (~p) has row p zeroed. A
 // position past the last row is passed over.
@@ -350,10 +346,11 @@ GradPlan grad_plan(int elt, int64_t width, int64_t n) {
     g.cpr = (width + g.chunk - 1) / g.chunk;
     g.lanes = g.cpr > 16 ? 64 : 16;
     g.slices = int((g.cpr + g.lanes - 1) / g.lanes);
-    // enough groups for the card's 8,192 waves, as far as segments of 4 go
+    // 2,048 groups or more as far as segments of 4 go: shorter segments leave more
+    // partial rows (16,384 tokens of 1,024 bf16 57 us at 8,192 groups, 50 at 2,048)
     const int most = g.lanes, least = 4;
     g.seg = least;
-    while (g.seg < most && n * g.slices >= int64_t(2 * g.seg) * 8192) g.seg *= 2;
+    while (g.seg < most && n * g.slices >= int64_t(2 * g.seg) * 2048) g.seg *= 2;
     g.segs = (n + g.seg - 1) / g.seg;
     return g;
 }
@@ -377,42 +374,20 @@ GradWs carve_grad(int elt, int64_t n_rows, int64_t width, int64_t n, void *base)
         return r;
     };
     const GradPlan g = grad_plan(elt, width, n);
-    const bool sorted = n > kRankMax;  // by passes, through a second copy
+    const bool sorted = n > kRankMax;  // through a second copy
     for (int i = 0; i < 2; ++i) {
         w.keys[i] = reinterpret_cast<uint32_t *>(take(i == 0 || sorted ? size_t(n) * 4 : 0));
         w.pay[i] = reinterpret_cast<int *>(take(i == 0 || sorted ? size_t(n) * 4 : 0));
     }
     w.counts = reinterpret_cast<int *>(
-        take(sorted ? (size_t(4) * bin_blocks(n)) << passes_for(n_rows).bits : 0));
+        take(n > kMergeMax ? (size_t(4) * bin_blocks(n)) << passes_for(n_rows).bits : 0));
     w.listed = reinterpret_cast<int *>(take(4));
     w.list = reinterpret_cast<int *>(take(size_t(g.segs) * 4));
-    w.ld_part = g.cpr * g.chunk;
+    w.ld_part = int64_t(g.slices) * g.lanes * g.chunk;
     w.part = take(g.segs > 1 ? 2 * size_t(g.segs) * size_t(w.ld_part) * (elt == VSPMM_ELT_F64 ? 8 : 4) : 0);
     w.bytes = at;
     return w;
 }
-
-// Hands out the units of the table's rows that the gradient's launches zero:
-// each takes about as many bytes as its other blocks leave time for, the sums'
-// launch what is left.
-struct ZeroPlan {
-    ZeroRows rows;
-    int64_t next = 0, units = 0;
-    ZeroShare take(int64_t bytes) {
-        ZeroShare z;
-        z.rows = rows;
-        z.lo = next;
-        if (units > 0) {
-            const int64_t unit = int64_t(rows.row_bytes) * rows.unit_rows;
-            next = std::min(units, next + (bytes + unit - 1) / unit);
-        }
-        z.hi = next;
-        return z;
-    }
-};
-constexpr int64_t kMB = 1 << 20;
-constexpr int64_t kZeroRank = 16 * kMB, kZeroCount = 24 * kMB, kZeroPlace = 48 * kMB,
-                  kZeroJoin = 24 * kMB;
 
 vspmm_status check_rows(int64_t n, int64_t width, int64_t ld, const void *p) {
     if (!fits(n) || !fits(width) || ld < 0) return VSPMM_ERR_DIM;
@@ -429,13 +404,14 @@ vspmm_status check_out(int64_t n, int64_t width, int64_t ld, const void *p) {
 template <typename T, typename G, bool ADD>
 void launch_grad(const GradPlan &g, const GradWs &w, const uint32_t *keys, const int *order,
                  int64_t n, int64_t n_rows, const void *dout, int64_t ld_dout, int64_t width,
-                 double scale, void *grad, int64_t ld_grad, ZeroPlan &zero, hipStream_t s) {
+                 double scale, void *grad, int64_t ld_grad, hipStream_t s) {
     using A = typename Sum<T>::type;
     GradArgs<T, G> a;
     a.keys = keys;
     a.order = order;
     a.n = int(n);
     a.seg = g.seg;
+    a.segs = int(g.segs);
     a.n_rows = uint32_t(n_rows);
     a.dout = static_cast<const T *>(dout);
     a.ld_dout = ld_dout;
@@ -452,21 +428,13 @@ void launch_grad(const GradPlan &g, const GradWs &w, const uint32_t *keys, const
     a.listed = w.listed;
     auto go = [&](auto chunk, auto lanes) {
         constexpr int C = decltype(chunk)::value, L = decltype(lanes)::value, PER = kGradThreads / L;
-        constexpr int WAVES = kGradThreads / 64;
         const int64_t items = g.segs * g.slices;
-        const unsigned sum_blocks = unsigned((items + PER - 1) / PER);
-        const bool join = g.segs > 1;
-        const int64_t rest = (zero.units - zero.next) * int64_t(zero.rows.row_bytes) *
-                             zero.rows.unit_rows;
-        const ZeroShare z = zero.take(join ? rest - std::min(rest / 4, kZeroJoin) : rest);
-        hipLaunchKernelGGL((k_grad_rows<T, G, C, L, ADD>), dim3(sum_blocks + z.blocks(WAVES)),
-                           dim3(kGradThreads), 0, s, a, sum_blocks, z);
-        if (!join) return;
-        const ZeroShare zj = zero.take(rest);
-        const unsigned join_blocks = unsigned(std::min<int64_t>(items, 2048));
-        hipLaunchKernelGGL((k_grad_join<T, G, C, L, ADD>),
-                           dim3(join_blocks + zj.blocks(WAVES)), dim3(kGradThreads), 0, s,
-                           a, join_blocks, zj);
+        hipLaunchKernelGGL((k_grad_rows<T, G, C, L, ADD>), dim3(unsigned((items + PER - 1) / PER)),
+                           dim3(kGradThreads), 0, s, a);
+        if (g.segs > 1)
+            hipLaunchKernelGGL((k_grad_join<T, G, C, L, ADD>),
+                               dim3(unsigned(std::min<int64_t>(items, 2048))), dim3(kJoinThreads), 0, s,
+                               a);
     };
     const std::integral_constant<int, 64> wide;
     const std::integral_constant<int, 16> narrow;
@@ -538,20 +506,15 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
     if (need > 0 && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255)))
         return VSPMM_ERR_WORKSPACE;
     if (n_rows == 0 || width == 0) return VSPMM_OK;
-    ZeroPlan zero;
-    if (!accumulate) {
-        // nontemporal zeroing beside many rows of dout (16,384 tokens, 131,072
-        // rows of 2,048 bf16: 142 -> 130 us), plain where zeroing is nearly all
-        // there is (2,048 tokens, 64,000 rows of 1,024 f32: 60 -> 49 us)
-        zero.rows = ZeroRows(grad, ld_grad * elt_bytes(grad_elt), n_rows, width * elt_bytes(grad_elt),
-                             8 * n >= n_rows);
-        zero.units = zero.rows.units();
-    }
+    // Every row is zeroed first, by blocks of the first launch beside its own
+    // (the sort's latency hides there), and the rows that tokens select written
+    // again: zeroing the others alone, later, mixes reads and writes and was slower.
+    ZeroRows zero;
+    if (!accumulate)
+        zero = ZeroRows(grad, ld_grad * elt_bytes(grad_elt), n_rows, width * elt_bytes(grad_elt));
     if (n == 0) {
-        if (accumulate) return VSPMM_OK;
-        const ZeroShare z = zero.take(int64_t(1) << 60);
-        hipLaunchKernelGGL(k_zero, dim3(z.blocks(kThreads / 64)), dim3(kThreads), 0, stream,
-                           z);
+        if (zero.chunks)
+            hipLaunchKernelGGL(k_zero, dim3(zero.blocks(kThreads)), dim3(kThreads), 0, stream, zero);
         return launched();
     }
     const GradPlan plan = grad_plan(elt, width, n);
@@ -561,11 +524,28 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
     with_index(index, [&](auto i) {
         using I = decltype(i);
         if (n <= kRankMax) {
-            const ZeroShare z = zero.take(kZeroRank);
             const int nb = int((n + kRankTile - 1) / kRankTile);
-            hipLaunchKernelGGL(k_rank<I>, dim3(nb + z.blocks(kRankThreads / 64)),
-                               dim3(kRankThreads), 0, stream, static_cast<const I *>(ids), int(n),
-                               n_rows, nb, PlaceKeys{w.keys[0], w.pay[0], nullptr}, w.listed, z);
+            hipLaunchKernelGGL(k_rank<I>, dim3(nb + zero.blocks(kRankThreads)), dim3(kRankThreads), 0,
+                               stream, static_cast<const I *>(ids), int(n), n_rows, nb,
+                               PlaceKeys{w.keys[0], w.pay[0], nullptr}, w.listed, zero);
+            return;
+        }
+        if (n <= kMergeMax) {
+            const int nb = int((n + kRankTile - 1) / kRankTile);
+            hipLaunchKernelGGL(k_chunk_rank<I>, dim3(nb + zero.blocks(kChunkThreads)),
+                               dim3(kChunkThreads), 0, stream, static_cast<const I *>(ids), int(n),
+                               n_rows, nb, PlaceKeys{w.keys[1], w.pay[1], nullptr}, w.listed, zero);
+            auto merge = [&](auto t) {
+                constexpr int TILE = decltype(t)::value;
+                allow_dynamic(reinterpret_cast<const void *>(&k_merge_rank<TILE>), kMergeLds<TILE>);
+                hipLaunchKernelGGL(k_merge_rank<TILE>, dim3((int(n) + TILE - 1) / TILE),
+                                   dim3(kMergeThreads), kMergeLds<TILE>, stream, w.keys[1], w.pay[1],
+                                   int(n), PlaceKeys{w.keys[0], w.pay[0], nullptr});
+            };
+            // a block for each of the 256 CUs, as far as tiles of 64 to 256 go
+            if (n <= 64 * 256) merge(std::integral_constant<int, 64>{});
+            else if (n <= 128 * 256) merge(std::integral_constant<int, 128>{});
+            else merge(std::integral_constant<int, 256>{});
             return;
         }
         const Passes ps = passes_for(n_rows);
@@ -574,15 +554,13 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
         auto pass = [&](auto *src, int k) {
             using S = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
             const BinPass<S> p{src, n, n_rows, k * ps.bits, bins, piece, nb};
-            ZeroShare z = zero.take(kZeroCount);
-            hipLaunchKernelGGL(k_bin_count<S>, dim3(nb + z.blocks(kBinWaves)),
-                               dim3(kBinThreads), size_t(bins) * 4, stream, p, w.counts, w.listed, z);
+            if (k > 0) zero = ZeroRows();
+            hipLaunchKernelGGL(k_bin_count<S>, dim3(nb + zero.blocks(kBinThreads)), dim3(kBinThreads),
+                               size_t(bins) * 4, stream, p, w.counts, w.listed, zero);
             allow_dynamic(reinterpret_cast<const void *>(&k_bin_place<S, PlaceKeys>), bin_lds(bins));
             const PlaceKeys to{w.keys[k & 1], w.pay[k & 1], order};
-            z = zero.take(kZeroPlace);
-            hipLaunchKernelGGL((k_bin_place<S, PlaceKeys>), dim3(nb + z.blocks(kBinWaves)),
-                               dim3(kBinThreads), bin_lds(bins), stream, p, ps.bits, w.counts, to,
-                               static_cast<int *>(nullptr), z);
+            hipLaunchKernelGGL((k_bin_place<S, PlaceKeys>), dim3(nb), dim3(kBinThreads), bin_lds(bins),
+                               stream, p, ps.bits, w.counts, to, static_cast<int *>(nullptr));
             keys = to.keys;
             order = to.pay;
         };
@@ -594,10 +572,10 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
         using G = decltype(g);
         if (accumulate)
             launch_grad<T, G, true>(plan, w, keys, order, n, n_rows, dout, ld_dout, width, scale, grad,
-                                    ld_grad, zero, stream);
+                                    ld_grad, stream);
         else
             launch_grad<T, G, false>(plan, w, keys, order, n, n_rows, dout, ld_dout, width, scale, grad,
-                                     ld_grad, zero, stream);
+                                     ld_grad, stream);
     };
     with_elt(elt, [&](auto e) {
         if (grad_elt == elt) sum(e, e);
@@ -629,10 +607,8 @@ vspmm_status vspmm_route(vspmm_index index, int64_t n_tokens, int64_t top_k, int
         return VSPMM_ERR_WORKSPACE;
     const int bins = int(n_experts) + 1;
     if (n == 0) {
-        ZeroShare z;
-        z.rows = ZeroRows(offsets, int64_t(bins) * 4, 1, int64_t(bins) * 4, false);
-        z.hi = 1;
-        hipLaunchKernelGGL(k_zero, dim3(1), dim3(kThreads), 0, stream, z);
+        const ZeroRows z(offsets, 0, 1, int64_t(bins) * 4);
+        hipLaunchKernelGGL(k_zero, dim3(z.blocks(kThreads)), dim3(kThreads), 0, stream, z);
         return launched();
     }
     const int piece = bin_piece(n), nb = bin_blocks(n);
@@ -642,11 +618,10 @@ vspmm_status vspmm_route(vspmm_index index, int64_t n_tokens, int64_t top_k, int
         const BinPass<I> p{static_cast<const I *>(experts), n, n_experts, -1, bins, piece, nb};
         if (nb > 1)
             hipLaunchKernelGGL(k_bin_count<I>, dim3(nb), dim3(kBinThreads), size_t(bins) * 4, stream,
-                               p, counts, static_cast<int *>(nullptr), ZeroShare{});
+                               p, counts, static_cast<int *>(nullptr), ZeroRows());
         allow_dynamic(reinterpret_cast<const void *>(&k_bin_place<I, PlaceRoute>), bin_lds(bins));
         hipLaunchKernelGGL((k_bin_place<I, PlaceRoute>), dim3(nb), dim3(kBinThreads), bin_lds(bins),
-                           stream, p, bits_of(n_experts), counts, PlaceRoute{order, position}, offsets,
-                           ZeroShare{});
+                           stream, p, bits_of(n_experts), counts, PlaceRoute{order, position}, offsets);
     });
     return launched();
 }

@@ -232,8 +232,27 @@ def test_embedding_grad_exact_on_integers():
         dout = ints(rng, (n, w), F32, dev)
         dids = torch.from_numpy(ids).to(dev)
         grad = sdm().embedding_grad(dout, dids, v)
-        want = torch.zeros((v, w), dtype=F64, device=dev).index_add_(0, dids, dout.double())
-        assert torch.equal(grad.double(), want), (n, v, w)
+        want = np.stack([np.bincount(ids, weights=col, minlength=v) for col in R.f64(dout).T], axis=1)
+        assert np.array_equal(R.f64(grad), want), (n, v, w)
+
+
+@pytest.mark.parametrize("n", [8191, 8192, 8193, 16384, 16385, 32769, 65536, 65537, 300_000])
+@pytest.mark.parametrize("kind", ["uniform", "same", "zipf", "hot", "padded"])
+def test_embedding_grad_sort_paths(n, kind):
+    """Lists on both sides of every length where the sort's kind changes, in
+    tables of one, two and three digits: exact on integers, every row (a sum of
+    at most 300,000 products of at most 3 stays below 2^24)."""
+    dev = need_gpu()
+    rng = np.random.default_rng(n)
+    for v, w in ((7, 5), (50_021, 2), (5_000_000, 1)):
+        ids = token_ids(kind, n, v, rng)
+        dout = ints(rng, (n, w), F32, dev, high=3)
+        dids = torch.from_numpy(ids).to(dev)
+        grad = sdm().embedding_grad(dout, dids, v)
+        real = (ids >= 0) & (ids < v)
+        want = np.stack([np.bincount(ids[real], weights=col[real], minlength=v)
+                         for col in R.f64(dout).T], axis=1)
+        assert np.array_equal(R.f64(grad), want), (v, w)
 
 
 def test_embedding_grad_empty():
