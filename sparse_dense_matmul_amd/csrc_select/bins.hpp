@@ -32,8 +32,10 @@ constexpr int kBinMax = 4097;     // most bins (counters of 8 waves: 131,104 byt
 inline size_t bin_lds(int bins) { return size_t(kBinWaves) * (bins + 1) * 4; }
 
 // Elements per wave's piece: the least multiple of 64 that keeps the tiles
-// within kBinBlocks.
+// within kBinBlocks; one tile, and so one launch, for up to 4,096 elements.
 inline int bin_piece(int64_t n) {
+    if (n <= 2 * kBinPiece * kBinWaves)
+        return n <= 0 ? 64 : int((n + kBinWaves * 64 - 1) / (kBinWaves * 64)) * 64;
     const int64_t per = (n + int64_t(kBinBlocks) * kBinWaves - 1) / (int64_t(kBinBlocks) * kBinWaves);
     const int64_t p = (per + 63) / 64 * 64;
     return int(p < kBinPiece ? kBinPiece : p);
@@ -352,8 +354,7 @@ constexpr int kMergeStage = 16;
 constexpr int kMergeMax = 65536;  // most elements: a pass over as many tokens takes 42 us,
                                   // by digits 44; over twice as many 74 and 51
 
-template <int TILE>
-constexpr size_t kMergeLds = size_t(kMergeStage * kChunkKeys + TILE) * 4;
+constexpr size_t kMergeLds = size_t(kMergeStage * kChunkKeys) * 4;  // 64 KB
 
 template <int TILE>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -362,13 +363,11 @@ k_merge_rank(const uint32_t *__restrict__ chunk_keys, const int *__restrict__ ch
     constexpr int SLOTS = kMergeThreads / TILE, PER = kMergeStage / SLOTS;
     constexpr int QUADS = kMergeStage * kChunkKeys / 4 / kMergeThreads;  // a thread's of a stage
     extern __shared__ __align__(16) uint32_t keys[];
-    int *const place = reinterpret_cast<int *>(keys + kMergeStage * kChunkKeys);  // [TILE]
     const int tid = threadIdx.x;
     const int e = blockIdx.x * TILE + (tid & (TILE - 1));
     const int slot = tid / TILE;
     const uint32_t key = e < n ? chunk_keys[e] : 0u;
     const int home = e / kChunkKeys, chunks = (n + kChunkKeys - 1) / kChunkKeys;
-    if (tid < TILE) place[tid] = e & (kChunkKeys - 1);
     uint4 next[QUADS];
     auto fetch = [&](int c0) {  // past the list: above every key
 #pragma unroll
@@ -411,6 +410,10 @@ k_merge_rank(const uint32_t *__restrict__ chunk_keys, const int *__restrict__ ch
             if (c0 + j * SLOTS + slot != home) sum += at[j] - (j * SLOTS + slot) * kChunkKeys;
         }
     }
+    __syncthreads();
+    int *const place = reinterpret_cast<int *>(keys);  // [TILE]
+    if (tid < TILE) place[tid] = e & (kChunkKeys - 1);
+    __syncthreads();
     if (sum) atomicAdd(&place[tid & (TILE - 1)], sum);
     __syncthreads();
     if (tid < TILE && e < n) out.put(e, place[tid], key, chunk_pay[e], 0);

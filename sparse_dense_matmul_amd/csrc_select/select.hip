@@ -13,7 +13,6 @@
 #include "vspmm.h"
 #include "bins.hpp"
 #include "grad.hpp"
-#include "../csrc/launch.hpp"
 #include "rows.hpp"
 
 using namespace vspmm;
@@ -314,8 +313,10 @@ bool streams(int64_t n, int64_t width, int elt) {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// Lets a kernel of the current device use that much dynamic LDS.
 void allow_dynamic(const void *fn, size_t bytes) {
-    if (bytes > 64 * 1024) allow_lds(fn);
+    if (bytes > 64 * 1024)
+        (void)hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
 int bits_of(int64_t x) {  // bits that hold 0 .. x
@@ -537,9 +538,8 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
                                n_rows, nb, PlaceKeys{w.keys[1], w.pay[1], nullptr}, w.listed, zero);
             auto merge = [&](auto t) {
                 constexpr int TILE = decltype(t)::value;
-                allow_dynamic(reinterpret_cast<const void *>(&k_merge_rank<TILE>), kMergeLds<TILE>);
                 hipLaunchKernelGGL(k_merge_rank<TILE>, dim3((int(n) + TILE - 1) / TILE),
-                                   dim3(kMergeThreads), kMergeLds<TILE>, stream, w.keys[1], w.pay[1],
+                                   dim3(kMergeThreads), kMergeLds, stream, w.keys[1], w.pay[1],
                                    int(n), PlaceKeys{w.keys[0], w.pay[0], nullptr});
             };
             // a block for each of the 256 CUs, as far as tiles of 64 to 256 go

@@ -255,6 +255,25 @@ def test_embedding_grad_sort_paths(n, kind):
         assert np.array_equal(R.f64(grad), want), (v, w)
 
 
+def test_embedding_grad_nonfinite():
+    """A token's non-finite gradient reaches its own row of the table alone,
+    whatever stands beside it in the sorted list, and a dropped token's none."""
+    dev = need_gpu()
+    rng = np.random.default_rng(14)
+    for n, w in ((40, 33), (3000, 520)):
+        ids = np.sort(rng.integers(0, 200, n))[rng.permutation(n)]
+        ids[:3] = [5, 6, -1]
+        ids[3:][(ids[3:] == 5) | (ids[3:] == 6)] = 7
+        dout = torch.ones((n, w), dtype=BF16, device=dev)
+        dout[0], dout[1], dout[2] = float("nan"), float("inf"), float("nan")
+        grad = sdm().embedding_grad(dout, torch.from_numpy(ids).to(dev), 200)
+        assert grad[5].isnan().all() and (grad[6] == float("inf")).all()
+        rest = torch.cat([grad[:5], grad[7:]])
+        count = np.bincount(ids[3:], minlength=200)
+        want = torch.from_numpy(np.delete(count, [5, 6])).to(dev).to(BF16)
+        assert torch.equal(rest, want[:, None].expand(198, w))
+
+
 def test_embedding_grad_empty():
     dev = need_gpu()
     none = torch.zeros(0, dtype=torch.int64, device=dev)
@@ -462,13 +481,13 @@ def test_on_another_stream():
     assert same_bits(out, want) and same_bits(grad, want_grad)
 
 
-@pytest.mark.parametrize("t", [16, 1500])
-def test_captured_graph(t):
+@pytest.mark.parametrize("t,e", [(16, 12), (1500, 12), (9000, 3000)])
+def test_captured_graph(t, e):
     """One training step's calls in a graph, replayed on new inputs: every
     replay gives the eager bits."""
     dev = need_gpu()
     rng = np.random.default_rng(t)
-    v, w, e, k = 700, 260, 12, 4
+    v, w, k = 700, 260, 4
     table = normal(rng, (v, w), BF16, dev)
     ids = torch.zeros(t, dtype=torch.int64, device=dev)
     experts = torch.zeros((t, k), dtype=torch.int64, device=dev)

@@ -75,6 +75,8 @@ def test_route_statuses():
         assert size(*args, ctypes.byref(n)) == DIM
     assert size(4, 2, 4097, ctypes.byref(n)) == UNSUPPORTED
     assert size(4, 2, 4096, ctypes.byref(n)) == 0
+    for args in ((0, 4, 9), (4, 0, 9), (0, 0, 0)):
+        assert size(*args, ctypes.byref(n)) == 0
     assert size(4, 2, 8, ctypes.byref(n)) == 0
     need = n.value
     f = sdm.lib.vspmm_route
