@@ -551,8 +551,8 @@ vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows,
                               int64_t ld_dout, double scale, int32_t accumulate, void *grad,
                               int64_t ld_grad, void *ws, size_t ws_bytes, hipStream_t stream);
 
-/* Workspace bytes of vspmm_embed_grad; elt is dout's type. bytes: host.
- * Errors: _NULL, _ENUM, _DIM. */
+/* Workspace bytes of vspmm_embed_grad; elt is dout's type. Enough for every
+ * smaller n, too. bytes: host. Errors: _NULL, _ENUM, _DIM, _UNSUPPORTED. */
 vspmm_status vspmm_embed_grad_workspace_size(vspmm_elt elt, int64_t n_rows, int64_t width,
                                              int64_t n, size_t *bytes);
 
@@ -571,6 +571,8 @@ vspmm_status vspmm_embed_grad_workspace_size(vspmm_elt elt, int64_t n_rows, int6
 vspmm_status vspmm_route(vspmm_index index, int64_t n_tokens, int64_t top_k, int64_t n_experts,
                          const void *experts, int32_t *order, int32_t *position, int32_t *offsets,
                          void *ws, size_t ws_bytes, hipStream_t stream);
+/* Workspace bytes of vspmm_route, enough for fewer tokens, too. bytes: host.
+ * Errors: _NULL, _DIM, _UNSUPPORTED. */
 vspmm_status vspmm_route_workspace_size(int64_t n_tokens, int64_t top_k, int64_t n_experts,
                                         size_t *bytes);
 

@@ -131,9 +131,7 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
     ids = _index(ids, "ids", dev)
     n, (v, w) = ids.numel(), table.shape
     if out is None:
-        shape = (*ids.shape, w)
-        out = result = torch.empty(shape, dtype=table.dtype, device=dev)
-        ld_out = w
+        result, ld_out = table.new_empty(*ids.shape, w), w
     else:
         result, ld_out = _rows(out, "out", (n, w), table.dtype, dev, write=True)
     _call(dev, "vspmm_embed", lib.vspmm_embed, ELTS[table.dtype], v, w, table.data_ptr(), ld,
@@ -175,8 +173,7 @@ def embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, n_rows: int, scale
         dtype = dtype or grad_out.dtype
         if dtype not in ELTS:
             raise TypeError(f"dtype must be one of {list(ELTS)}, got {dtype}")
-        out = torch.empty((n_rows, w), dtype=dtype, device=dev)
-        ld_out = w
+        out, ld_out = grad_out.new_empty(n_rows, w, dtype=dtype), w
     else:
         out, ld_out = _rows(out, "out", (n_rows, w), dtype, dev, write=True)
     ws, ws_bytes = _workspace(need, workspace, dev)
@@ -203,7 +200,7 @@ def route(experts: torch.Tensor, n_experts: int,
            "vspmm_route_workspace_size")
     ws, ws_bytes = _workspace(int(need.value), workspace, dev)
     order = torch.empty(t * k, dtype=torch.int32, device=dev)
-    position = torch.empty((t, k), dtype=torch.int32, device=dev)
+    position = torch.empty(t, k, dtype=torch.int32, device=dev)
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
     _call(dev, "vspmm_route", lib.vspmm_route, INDICES[experts.dtype], t, k, n_experts,
           experts.data_ptr(), order.data_ptr(), position.data_ptr(), offsets.data_ptr(),
@@ -224,7 +221,7 @@ def dispatch(x: torch.Tensor, position: torch.Tensor,
     if x.shape[0] != t:
         raise ValueError(f"x has {x.shape[0]} rows, position {t}")
     if out is None:
-        out, ld_out = torch.empty((t * k, w), dtype=x.dtype, device=dev), w
+        out, ld_out = x.new_empty(t * k, w), w
     else:
         out, ld_out = _rows(out, "out", (t * k, w), x.dtype, dev, write=True)
     _call(dev, "vspmm_dispatch", lib.vspmm_dispatch, ELTS[x.dtype], t, k, w, x.data_ptr(), ld,
@@ -243,7 +240,7 @@ def _sum_back(rows, position, weights, weighted, out):
     if weighted:
         weights = _weights(weights, (t, k), rows.dtype, dev)
     if out is None:
-        out, ld_out = torch.empty((t, w), dtype=rows.dtype, device=dev), w
+        out, ld_out = rows.new_empty(t, w), w
     else:
         out, ld_out = _rows(out, "out", (t, w), rows.dtype, dev, write=True)
     _call(dev, "vspmm_combine", lib.vspmm_combine, ELTS[rows.dtype], t, k, w, rows.data_ptr(), ld,
@@ -281,10 +278,10 @@ def combine_grad(grad_out: torch.Tensor, rows: torch.Tensor, position: torch.Ten
     grad_out, ld_grad_out = _rows(grad_out, "grad_out", (t, w), dtype, dev)
     weights = _weights(weights, (t, k), dtype, dev)
     if out is None:
-        out, ld_out = torch.empty((t * k, w), dtype=dtype, device=dev), w
+        out, ld_out = rows.new_empty(t * k, w), w
     else:
         out, ld_out = _rows(out, "out", (t * k, w), dtype, dev, write=True)
-    grad_weights = torch.empty((t, k), dtype=weights.dtype, device=dev)
+    grad_weights = weights.new_empty(t, k)
     _call(dev, "vspmm_combine_grad", lib.vspmm_combine_grad, ELTS[dtype], t, k, w,
           grad_out.data_ptr(), ld_grad_out, rows.data_ptr(), ld, position.data_ptr(),
           weights.data_ptr(), out.data_ptr(), ld_out, grad_weights.data_ptr())

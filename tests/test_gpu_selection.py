@@ -110,6 +110,15 @@ def test_embedding_empty():
     assert out.shape == (3, 8) and not out.any()
 
 
+def test_embedding_of_one_id_without_dimensions():
+    dev = need_gpu()
+    table = torch.arange(12.0, device=dev).reshape(4, 3)
+    one = torch.tensor(2, device=dev)
+    assert sdm().embedding(table, one).tolist() == [6, 7, 8]
+    grad = sdm().embedding_grad(torch.ones(3, device=dev), one, 4)
+    assert grad.tolist() == [[0, 0, 0], [0, 0, 0], [1, 1, 1], [0, 0, 0]]
+
+
 def test_embedding_nonfinite():
     """Non-finite entries reach the tokens that select them and no other."""
     dev = need_gpu()
@@ -457,6 +466,18 @@ def test_combine_is_the_csr_product():
     assert torch.equal(ones.spmm(x, "BA"), sdm().dispatch(x, r.position))
 
 
+def test_the_same_expert_twice_and_one_expert_for_all():
+    """Equal experts of one token are separate slots; one expert holding every
+    slot keeps their order."""
+    dev = need_gpu()
+    x = np.array([[3, 3], [1, 3], [3, 3]])
+    r = sdm().route(torch.from_numpy(x).to(dev), 5)
+    assert r.order.tolist() == [2, 0, 1, 3, 4, 5] and r.offsets.tolist() == [0, 0, 1, 1, 6, 6]
+    rows = torch.ones((6, 9), device=dev)
+    out = sdm().combine(rows, r.position, torch.tensor([[1.0, 2], [3, 4], [5, 6]], device=dev))
+    assert out[:, 0].tolist() == [3, 7, 11]
+
+
 # ------------------------------------------------- streams, graphs, refusals
 
 
@@ -523,6 +544,50 @@ def test_captured_graph(t, e):
         torch.cuda.synchronize()
         for a, b in zip(captured, step()):
             assert same_bits(a, b)
+
+
+def test_calls_on_two_streams_at_once():
+    """The same operators on two streams, each with its own workspace, while
+    both run: the bits of one after the other."""
+    dev = need_gpu()
+    rng = np.random.default_rng(61)
+    ids = [torch.from_numpy(token_ids("zipf", 20_000, 5000, rng)).to(dev) for _ in range(2)]
+    dout = [normal(rng, (20_000, 256), BF16, dev) for _ in range(2)]
+    experts = [torch.from_numpy(rng.integers(0, 64, (20_000, 2))).to(dev) for _ in range(2)]
+
+    def work(i):
+        r = sdm().route(experts[i], 64)
+        rows = sdm().dispatch(dout[i], r.position)
+        return sdm().embedding_grad(dout[i], ids[i], 5000), r.position, rows
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for result in got[i]:
+            for a, b in zip(result, want[i]):
+                assert same_bits(a, b)
+
+
+def test_workspace_given():
+    """A caller's workspace, filled with ones before each call, serves calls of
+    any smaller size after one another."""
+    dev = need_gpu()
+    rng = np.random.default_rng(62)
+    ws = torch.empty(sdm().embedding_grad_workspace(400, 300, 9000, BF16), dtype=torch.uint8,
+                     device=dev)
+    for n in (9000, 8000, 100, 8500):
+        ids = torch.from_numpy(token_ids("hot", n, 400, rng)).to(dev)
+        dout = normal(rng, (n, 300), BF16, dev)
+        ws.fill_(255)
+        got = sdm().embedding_grad(dout, ids, 400, workspace=ws)
+        assert same_bits(got, sdm().embedding_grad(dout, ids, 400)), n
 
 
 def test_refusals_on_the_device():

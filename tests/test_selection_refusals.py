@@ -150,3 +150,33 @@ def test_binding_refusals():
     with pytest.raises(sdm.VspmmError) as e:
         sdm.embedding_grad_workspace(-1, 8, 4, torch.float32)
     assert e.value.status == DIM
+
+
+@pytest.mark.parametrize("width", [1, 7, 64, 300, 1024, 4096, 20_000])
+def test_workspaces_do_not_shrink(width):
+    """A workspace for n tokens serves every shorter list: the size does not
+    fall as n grows, also where the sort or the segments change."""
+    size, n = sdm.lib.vspmm_embed_grad_workspace_size, ctypes.c_size_t()
+    lengths = sorted({*range(1, 300, 7), *(2**k + d for k in range(5, 22) for d in (-1, 0, 1)),
+                      *range(4000, 140_000, 777)})
+    for elt in (0, 1, 2):
+        last = 0
+        for t in lengths:
+            assert size(elt, 50_000, width, t, ctypes.byref(n)) == 0
+            assert n.value >= last, (elt, t)
+            last = n.value
+    last = 0
+    for t in lengths:
+        assert sdm.lib.vspmm_route_workspace_size(t, 3, 500, ctypes.byref(n)) == 0
+        assert n.value >= last, t
+        last = n.value
+
+
+def test_workspace_follows_documented_limits():
+    size, n = sdm.lib.vspmm_embed_grad_workspace_size, ctypes.c_size_t()
+    assert size(2, 100, 64, 2**28, ctypes.byref(n)) == 0
+    assert size(2, 100, 64, 2**30, ctypes.byref(n)) == UNSUPPORTED
+    assert size(2, 100, 512, 2**30, ctypes.byref(n)) == 0
+    assert size(2, 100, 2**24 + 1, 4, ctypes.byref(n)) == UNSUPPORTED
+    f = sdm.lib.vspmm_embed
+    assert f(2, 10, 2**24 + 1, D, 2**25, 0, 4, D, 1.0, D, 2**25, None) == UNSUPPORTED
