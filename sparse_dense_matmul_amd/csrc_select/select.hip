@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int64_t kI32Max = 2147483647;
+constexpr int kNoRow = 2147483647;  // a position past every row: slots number at most this
 // k_embed: four chunks a lane from here on, with nontemporal stores (16,384 rows of
 // 4,096 bf16 48 -> 34 us); one below, for as many waves as there are chunks
 constexpr uint32_t kManyChunks = 1 << 20;
@@ -36,6 +37,19 @@ __device__ __forceinline__ void by_eights(int n, F &&f) {
     if (n & 4) f(std::integral_constant<int, 4>{}, k), k += 4;
     if (n & 2) f(std::integral_constant<int, 2>{}, k), k += 2;
     if (n & 1) f(std::integral_constant<int, 1>{}, k);
+}
+
+// f(count, k, m): eight at a time, then all that are left in one batch of the
+// least power of two that holds them, m of which count.
+template <typename F>
+__device__ __forceinline__ void by_padded_eights(int n, F &&f) {
+    int k = 0;
+    for (; k + 8 <= n; k += 8) f(std::integral_constant<int, 8>{}, k, 8);
+    const int m = n - k;
+    if (m > 4) f(std::integral_constant<int, 8>{}, k, m);
+    else if (m > 2) f(std::integral_constant<int, 4>{}, k, m);
+    else if (m > 1) f(std::integral_constant<int, 2>{}, k, m);
+    else if (m > 0) f(std::integral_constant<int, 1>{}, k, m);
 }
 
 // The chunks of a batch of rows as one flat list: consecutive lanes take
@@ -209,7 +223,7 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
     const uint32_t t = blockIdx.x * PER + mine;
     const bool real = t < n_tokens;
     const int64_t slot0 = int64_t(t) * top_k;
-    auto batch = [&](auto count, int k) {
+    auto batch = [&](auto count, int k, int m) {
         constexpr int N = decltype(count)::value;
         A dot[N] = {};
         if (real) {
@@ -219,10 +233,10 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
             const T *from[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int p = position[slot0 + k + j];
+                const int p = j < m ? position[slot0 + k + j] : kNoRow;
                 row[j] = uint32_t(p >= 0 ? p : ~p);
                 kept[j] = p >= 0 && row[j] < n_slots;
-                w[j] = weight[slot0 + k + j];
+                w[j] = j < m ? weight[slot0 + k + j] : A(0);
                 from[j] = kept[j] ? rows + int64_t(row[j]) * ld_rows : dout + int64_t(t) * ld_dout;
             }
             for (uint32_t c = part * 64 + lane; c < cpr; c += 64 * W) {
@@ -254,12 +268,13 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
         const A total = wave_totals(dot, lane);
         constexpr int SPAN = 64 / N;  // lanes that hold one value's total
         if (W == 1) {
-            if (real && lane % SPAN == 0) grad_weight[slot0 + k + lane / SPAN] = total;
+            if (real && lane % SPAN == 0 && lane / SPAN < m)
+                grad_weight[slot0 + k + lane / SPAN] = total;
             return;
         }
         if (lane % SPAN == 0) sums[mine][part][lane / SPAN] = total;
         __syncthreads();
-        if (real && part == 0 && lane < N) {
+        if (real && part == 0 && lane < m) {
             A all = sums[mine][0][lane];
 #pragma unroll
             for (int w2 = 1; w2 < W; ++w2) all += sums[mine][w2][lane];
@@ -267,7 +282,10 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
         }
         __syncthreads();
     };
-    by_eights(top_k, batch);
+    // one batch for five to seven slots, not two or three: each has a round of
+    // loads and two barriers of its own (six slots of 1,001 f32 54 -> 47 us with the
+    // gradient of the dispatch; the combine, without barriers, gains nothing so)
+    by_padded_eights(top_k, batch);
 }
 
 // --------------------------------------------------------------------- host

@@ -373,7 +373,8 @@ def routed(t, k, e, drop, rng, dev):
 def test_dispatch_combine_and_gradients(dtype, width):
     dev = need_gpu()
     for t, k, e, drop in ((1, 1, 4, 0.0), (1, 8, 16, 0.4), (33, 4, 8, 0.0), (50, 9, 12, 0.3),
-                          (7, 17, 40, 0.0), (9, 2, 3, 1.0)):
+                          (7, 17, 40, 0.0), (9, 2, 3, 1.0), (10, 3, 5, 0.1), (11, 5, 9, 0.2),
+                          (8, 6, 8, 0.25), (6, 7, 9, 0.0)):
         rng = np.random.default_rng(t + width)
         r, pos = routed(t, k, e, drop, rng, dev)
         n = t * k
