@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -11,6 +12,20 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (runs through the HIP library)")
     config.addinivalue_line("markers", "slow: full-size workloads (minutes of host time)")
+
+
+def pytest_collection_finish(session):
+    # what the imports made stays: later collections pass over it quickly
+    gc.collect()
+    gc.freeze()
+
+
+def pytest_runtest_setup(item):
+    """Device memory that an earlier test left in a reference cycle (an exception
+    kept by pytest.raises holds its frames) is freed before the next GPU test,
+    not at some allocation inside one that counts device bytes."""
+    if item.get_closest_marker("gpu"):
+        gc.collect()
 
 
 @pytest.fixture(scope="session")
