@@ -147,6 +147,20 @@ def test_embedding_past_2_31_elements():
     assert int(grad.any(dim=1).sum()) == 4
 
 
+def test_embedding_of_more_chunks_than_a_launch_takes():
+    """300,000 x 65,536 bf16 (39 GB) out: 2.4e9 chunks, two launches, the second
+    from row 262,016 on."""
+    dev = need_gpu()
+    n, w = 300_000, 65_536
+    table = torch.arange(1, 6, device=dev).to(BF16)[:, None].expand(5, w).contiguous()
+    ids = torch.arange(n, device=dev) % 6  # 5 is outside
+    out = sdm().embedding(table, ids)
+    want = torch.where(ids < 5, ids + 1, 0).to(BF16)
+    for a, b in ((0, 50), (262_000, 262_050), (n - 50, n)):
+        assert torch.equal(out[a:b], want[a:b, None].expand(b - a, w)), a
+    assert torch.equal(out[:, w - 1], want) and torch.equal(out[:, 0], want)
+
+
 # ---------------------------------------------------------- embedding grad
 
 
@@ -405,6 +419,18 @@ def test_dispatch_combine_and_gradients(dtype, width):
         # the same bits again
         gr2, gw2 = sdm().combine_grad(dout, rows, r.position, weights)
         assert same_bits(gr, gr2) and same_bits(gw, gw2)
+
+
+def test_combine_grad_of_more_tokens_than_a_launch_takes():
+    """5,000,000 tokens of one expert each, in two launches."""
+    dev = need_gpu()
+    t = 5_000_000
+    pos = torch.arange(t - 1, -1, -1, device=dev, dtype=torch.int32)[:, None].contiguous()
+    rows = (torch.arange(t, device=dev) % 1000).float()[:, None].expand(t, 4).contiguous()
+    dout = (torch.arange(t, device=dev) % 7).float()[:, None].expand(t, 4)
+    gr, gw = sdm().combine_grad(dout, rows, pos, torch.full((t, 1), 2.0, device=dev))
+    assert torch.equal(gr, 2 * dout.flip(0))
+    assert torch.equal(gw[:, 0], 4 * dout[:, 0] * rows[:, 0].flip(0))
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=by_name)
