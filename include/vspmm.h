@@ -509,7 +509,8 @@ vspmm_status vspmm_plan_info(vspmm_matrix h, int64_t width, vspmm_direction dir,
  *    other array of the call.
  *  - Sums and products run in float32 for VSPMM_ELT_F32, _BF16 and _F16 and in
  *    float64 for VSPMM_ELT_F64, and are rounded once (to nearest even) to the
- *    type written. Weights are float32 (float64 for VSPMM_ELT_F64).
+ *    type written. Weights are float32 (float64 for VSPMM_ELT_F64); scale is
+ *    rounded to that type first.
  *  - Indices outside their range are legal: such a row of the matrix has no
  *    entry (padding, or rows and experts held by another device), so it selects
  *    nothing and its output is zero. Nothing is read or written out of bounds

@@ -469,6 +469,10 @@ void launch_grad(const GradPlan &g, const GradWs &w, const uint32_t *keys, const
         const int64_t items = g.segs * g.slices;
         hipLaunchKernelGGL((k_grad_rows<T, G, C, L, ADD>), dim3(unsigned((items + PER - 1) / PER)),
                            dim3(kGradThreads), 0, s, a);
+        if (g.segs >= kFoldSegs)
+            hipLaunchKernelGGL((k_grad_fold<T, G, C, L>),
+                               dim3(unsigned(g.segs / kFold), unsigned(g.slices)), dim3(kJoinThreads),
+                               0, s, a);
         if (g.segs > 1)
             hipLaunchKernelGGL((k_grad_join<T, G, C, L, ADD>),
                                dim3(unsigned(std::min<int64_t>(items, 2048))), dim3(kJoinThreads), 0, s,

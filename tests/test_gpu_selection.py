@@ -278,6 +278,28 @@ def test_embedding_grad_sort_paths(n, kind):
         assert np.array_equal(R.f64(grad), want), (v, w)
 
 
+@pytest.mark.parametrize("dtype,w", [(F32, 130), (F64, 5), (BF16, 600)])
+@pytest.mark.parametrize("kind", ["same", "hot", "zipf", "padded"])
+def test_embedding_grad_long_lists(kind, dtype, w):
+    """Lists long enough that a run's partial rows are folded before their join,
+    with runs that start and end anywhere in a block of folded segments: exact
+    on ones and zeros (counts below 2^24 in the float32 and float64 results)."""
+    dev = need_gpu()
+    n, v = 300_001, 2000
+    rng = np.random.default_rng(w)
+    ids = token_ids(kind, n, v, rng)
+    if kind == "padded":  # two long runs of odd lengths between short ones
+        ids[1000:150_777] = 900
+        ids[160_000:260_123] = 901
+    on = rng.integers(0, 2, n)
+    dout = torch.from_numpy(on).to(dev).to(dtype)[:, None].expand(n, w)
+    grad = sdm().embedding_grad(dout, torch.from_numpy(ids).to(dev), v,
+                                dtype=F64 if dtype == F64 else F32)
+    real = ids >= 0
+    want = np.bincount(ids[real], weights=on[real], minlength=v)
+    assert torch.equal(grad, torch.from_numpy(want).to(dev).to(grad.dtype)[:, None].expand(v, w))
+
+
 def test_embedding_grad_nonfinite():
     """A token's non-finite gradient reaches its own row of the table alone,
     whatever stands beside it in the sorted list, and a dropped token's none."""
