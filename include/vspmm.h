@@ -545,8 +545,7 @@ vspmm_status vspmm_embed(vspmm_elt elt, int64_t n_rows, int64_t width, const voi
  * and sizes: the result repeats bit for bit. ws: vspmm_embed_grad_workspace_size
  * bytes (may be NULL when that is 0). Errors: as vspmm_embed, plus _ENUM for
  * another pair of types, _WORKSPACE, _DIM for n_rows above 2^31 - 2 and
- * _UNSUPPORTED for more than 2^28 tokens (2^30 where rows are longer than 256
- * bytes, as far as n * width stays within 2^40 bytes). */
+ * _UNSUPPORTED for more than 2^30 tokens or dout of more than 2^40 bytes. */
 vspmm_status vspmm_embed_grad(vspmm_elt elt, vspmm_elt grad_elt, int64_t n_rows, int64_t width,
                               vspmm_index index, int64_t n, const void *ids, const void *dout,
                               int64_t ld_dout, double scale, int32_t accumulate, void *grad,

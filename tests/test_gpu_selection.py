@@ -259,7 +259,7 @@ def test_embedding_grad_exact_on_integers():
         assert np.array_equal(R.f64(grad), want), (n, v, w)
 
 
-@pytest.mark.parametrize("n", [8191, 8192, 8193, 16384, 16385, 32769, 65536, 65537, 300_000])
+@pytest.mark.parametrize("n", [8191, 8192, 8193, 16384, 16385, 32769, 65536, 65537, 131_071, 131_072, 300_000])
 @pytest.mark.parametrize("kind", ["uniform", "same", "zipf", "hot", "padded"])
 def test_embedding_grad_sort_paths(n, kind):
     """Lists on both sides of every length where the sort's kind changes, in

@@ -174,9 +174,11 @@ def test_workspaces_do_not_shrink(width):
 
 def test_workspace_follows_documented_limits():
     size, n = sdm.lib.vspmm_embed_grad_workspace_size, ctypes.c_size_t()
-    assert size(2, 100, 64, 2**28, ctypes.byref(n)) == 0
-    assert size(2, 100, 64, 2**30, ctypes.byref(n)) == UNSUPPORTED
+    assert size(2, 100, 64, 2**30, ctypes.byref(n)) == 0
     assert size(2, 100, 512, 2**30, ctypes.byref(n)) == 0
+    assert size(2, 100, 512, 2**30 + 1, ctypes.byref(n)) == UNSUPPORTED
+    assert size(2, 100, 2**14, 2**25, ctypes.byref(n)) == 0
+    assert size(2, 100, 2**14, 2**26, ctypes.byref(n)) == UNSUPPORTED
     assert size(2, 100, 2**24 + 1, 4, ctypes.byref(n)) == UNSUPPORTED
     f = sdm.lib.vspmm_embed
     assert f(2, 10, 2**24 + 1, D, 2**25, 0, 4, D, 1.0, D, 2**25, None) == UNSUPPORTED
