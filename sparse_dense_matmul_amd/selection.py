@@ -28,9 +28,15 @@ import torch
 
 from . import _check, lib
 
+
+def _public_raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 # the current stream's handle without the Stream object around it: 0.1 us where
-# torch.cuda.current_stream(device).cuda_stream takes 2, of a 10 us call
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the public way takes 2, of a 10 us call. A torch without this private function
+# takes the public way; importing the package needs neither.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
 __all__ = ["Routing", "combine", "combine_grad", "dispatch", "dispatch_grad", "embedding",
            "embedding_grad", "embedding_grad_workspace", "route"]
