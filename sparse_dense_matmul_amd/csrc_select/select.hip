@@ -367,6 +367,13 @@ Passes passes_for(int64_t limit) {
 }
 
 constexpr int64_t kGradGroups = 2048;
+// The longest list and the largest dout of the gradient. Within them there are
+// less than 2^26 pieces (segments times slices), which k_grad_rows numbers in 31
+// bits: a segment of less than 64 places means at most 2^13 pieces and a row's
+// slices, one of 64 at most 2^24 segments of one slice, or, where a row of more
+// than 1,008 bytes has several, less than two for each KB of it.
+constexpr int64_t kGradTokens = int64_t(1) << 30;
+constexpr int64_t kGradBytes = int64_t(1) << 40;
 
 // How k_grad_rows cuts the work: lanes per group, slices of the width, places
 // per segment.
@@ -534,8 +541,7 @@ vspmm_status vspmm_embed_grad_workspace_size(vspmm_elt elt, int64_t n_rows, int6
     if (!known_elt(elt)) return VSPMM_ERR_ENUM;
     if (!fits(n_rows) || n_rows == kI32Max || !fits(width) || !fits(n)) return VSPMM_ERR_DIM;
     if (width > kWidthMax) return VSPMM_ERR_UNSUPPORTED;
-    const GradPlan g = grad_plan(elt, width, n);
-    if (g.segs * g.slices > 1 << 24) return VSPMM_ERR_UNSUPPORTED;
+    if (n > kGradTokens || n * width * elt_bytes(elt) > kGradBytes) return VSPMM_ERR_UNSUPPORTED;
     *bytes = n_rows && width && n ? carve_grad(elt, n_rows, width, n, nullptr).bytes : 0;
     return VSPMM_OK;
 }
