@@ -16,7 +16,8 @@ Argument marshalling only, as in the rest of the binding: every gradient is a
 call of its own and nothing is recorded for autograd. Dense operands are
 bfloat16, float16, float32 or float64; rows may be strided (any row stride,
 elements of a row contiguous; others are copied). Ids and experts are int32 or
-int64, and values outside their range select nothing.
+int64, and values outside their range select nothing. A given ``out`` or
+``workspace`` shares no element with another array of its call (ValueError).
 """
 
 from __future__ import annotations
@@ -127,6 +128,50 @@ def _workspace(nbytes, workspace, device):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _region(t, ld=None):
+    """The bytes of a tensor's rows of stride ld (None: a contiguous tensor), as
+    (address, rows, bytes of a row, bytes from row to row)."""
+    if ld is None:
+        return t.data_ptr(), 1, t.nbytes, 0
+    (n, w), size = t.shape, t.element_size()
+    return t.data_ptr(), n, w * size, ld * size
+
+
+def _overlap(a, b):
+    """Whether two regions share a byte."""
+    (a0, na, wa, la), (b0, nb, wb, lb) = a, b
+    if not (na and wa and nb and wb):
+        return False
+    if a0 + (na - 1) * la + wa <= b0 or b0 + (nb - 1) * lb + wb <= a0:
+        return False
+    # rows without gaps are one row
+    if la <= wa:
+        na, wa = 1, (na - 1) * la + wa
+    if lb <= wb:
+        nb, wb = 1, (nb - 1) * lb + wb
+    if nb == 1:
+        a0, na, wa, la, b0, nb, wb, lb = b0, nb, wb, lb, a0, na, wa, la
+    if nb == 1:
+        return True
+    if na > 1 and la == lb:
+        # only the distance of two rows counts: the first one of a against all of them
+        b0, nb, na = b0 - (na - 1) * la, nb + na - 1, 1
+    for r in range(na):
+        at = a0 + r * la
+        q = max((at - b0 - wb) // lb + 1, 0)  # the first row of b that ends behind it
+        if q < nb and b0 + q * lb < at + wa:
+            return True
+    return False
+
+
+def _apart(name, written, **others):
+    """Refuses a written region (the caller's out or workspace) that overlaps
+    another array of the call: rows written by one wave may be read by another."""
+    for other, region in others.items():
+        if _overlap(written, region):
+            raise ValueError(f"{name} must not overlap {other}")
+
+
 def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
               out: torch.Tensor | None = None) -> torch.Tensor:
     """``scale * table[ids]``, shaped ``ids.shape + (width,)``; an id outside the
@@ -140,6 +185,7 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
         result, ld_out = table.new_empty(*ids.shape, w), w
     else:
         result, ld_out = _rows(out, "out", (n, w), table.dtype, dev, write=True)
+        _apart("out", _region(result, ld_out), table=_region(table, ld), ids=_region(ids))
     _call(dev, "vspmm_embed", lib.vspmm_embed, ELTS[table.dtype], v, w, table.data_ptr(), ld,
           INDICES[ids.dtype], n, ids.data_ptr(), scale, result.data_ptr(), ld_out)
     return result
@@ -182,7 +228,11 @@ def embedding_grad(grad_out: torch.Tensor, ids: torch.Tensor, n_rows: int, scale
         out, ld_out = grad_out.new_empty(n_rows, w, dtype=dtype), w
     else:
         out, ld_out = _rows(out, "out", (n_rows, w), dtype, dev, write=True)
+        _apart("out", _region(out, ld_out), grad_out=_region(grad_out, ld), ids=_region(ids))
     ws, ws_bytes = _workspace(need, workspace, dev)
+    if workspace is not None:
+        _apart("workspace", (ws.data_ptr(), 1, min(need, ws_bytes), 0),
+               grad_out=_region(grad_out, ld), ids=_region(ids), out=_region(out, ld_out))
     _call(dev, "vspmm_embed_grad", lib.vspmm_embed_grad, ELTS[grad_out.dtype], ELTS[out.dtype],
           n_rows, w, INDICES[ids.dtype], n, ids.data_ptr(), grad_out.data_ptr(), ld, scale,
           int(accumulate), out.data_ptr(), ld_out, ws.data_ptr() if ws is not None else None, ws_bytes)
@@ -205,6 +255,9 @@ def route(experts: torch.Tensor, n_experts: int,
     _check(lib.vspmm_route_workspace_size(t, k, n_experts, ctypes.byref(need)),
            "vspmm_route_workspace_size")
     ws, ws_bytes = _workspace(int(need.value), workspace, dev)
+    if workspace is not None:
+        _apart("workspace", (ws.data_ptr(), 1, min(need.value, ws_bytes), 0),
+               experts=_region(experts))
     order = torch.empty(t * k, dtype=torch.int32, device=dev)
     position = torch.empty(t, k, dtype=torch.int32, device=dev)
     offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
@@ -230,6 +283,7 @@ def dispatch(x: torch.Tensor, position: torch.Tensor,
         out, ld_out = x.new_empty(t * k, w), w
     else:
         out, ld_out = _rows(out, "out", (t * k, w), x.dtype, dev, write=True)
+        _apart("out", _region(out, ld_out), x=_region(x, ld), position=_region(position))
     _call(dev, "vspmm_dispatch", lib.vspmm_dispatch, ELTS[x.dtype], t, k, w, x.data_ptr(), ld,
           position.data_ptr(), out.data_ptr(), ld_out)
     return out
@@ -249,6 +303,9 @@ def _sum_back(rows, position, weights, weighted, out):
         out, ld_out = rows.new_empty(t, w), w
     else:
         out, ld_out = _rows(out, "out", (t, w), rows.dtype, dev, write=True)
+        _apart("out", _region(out, ld_out), rows=_region(rows, ld), position=_region(position))
+        if weighted:
+            _apart("out", _region(out, ld_out), weights=_region(weights))
     _call(dev, "vspmm_combine", lib.vspmm_combine, ELTS[rows.dtype], t, k, w, rows.data_ptr(), ld,
           position.data_ptr(), weights.data_ptr() if weighted else None, out.data_ptr(), ld_out)
     return out
@@ -287,6 +344,8 @@ def combine_grad(grad_out: torch.Tensor, rows: torch.Tensor, position: torch.Ten
         out, ld_out = rows.new_empty(t * k, w), w
     else:
         out, ld_out = _rows(out, "out", (t * k, w), dtype, dev, write=True)
+        _apart("out", _region(out, ld_out), grad_out=_region(grad_out, ld_grad_out),
+               rows=_region(rows, ld), position=_region(position), weights=_region(weights))
     grad_weights = weights.new_empty(t, k)
     _call(dev, "vspmm_combine_grad", lib.vspmm_combine_grad, ELTS[dtype], t, k, w,
           grad_out.data_ptr(), ld_grad_out, rows.data_ptr(), ld, position.data_ptr(),
