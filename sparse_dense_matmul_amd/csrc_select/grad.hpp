@@ -35,15 +35,15 @@ __device__ __forceinline__ void write_grad(G *g, const A *acc, A scale, uint32_t
         if (moved) {
 #pragma unroll
             for (int i = 0; i < C; ++i)
-                if (i >= int(moved)) g[i] = G(fma(acc[i], scale, A(g[i])));
+                if (i >= int(moved)) g[i] = rounded<G>(fma(acc[i], scale, A(g[i])));
             return;
         }
         const Vec<G, C> old = load_vec<C>(g);
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = G(fma(acc[i], scale, A(old[i])));
+        for (int i = 0; i < C; ++i) o[i] = rounded<G>(fma(acc[i], scale, A(old[i])));
     } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = G(acc[i] * scale);
+        for (int i = 0; i < C; ++i) o[i] = rounded<G>(acc[i] * scale);
     }
     store_vec<C>(g, o);
 }

@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace vspmm {
 
 using bf16 = __bf16;
@@ -25,6 +27,17 @@ template <>
 struct Sum<double> {
     using type = double;
 };
+
+// A finished sum or product rounded to the type written. The empty asm keeps the
+// compiler from contracting the operation before it with a float16's conversion
+// (v_fma_mixlo_f16), which it does in some instances and not in others: that adds
+// +0 to a product, which takes a zero's sign, and rounds the exact result straight
+// to float16, so that a halfway case would depend on the width.
+template <typename T, typename A>
+__device__ __forceinline__ T rounded(A x) {
+    if constexpr (std::is_same_v<T, f16>) asm("" : "+v"(x));
+    return T(x);
+}
 
 template <typename T>
 constexpr int kChunk = int(16 / sizeof(T));  // elements per 16-byte chunk
