@@ -14,6 +14,12 @@ from test_gpu_selection import BF16, F16, F32, F64, TYPES, by_name, guarded, gua
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def give_back():
+    yield
+    torch.cuda.empty_cache()
+
+
 def gen(dev, seed):
     return torch.Generator(device=dev).manual_seed(seed)
 
@@ -231,3 +237,166 @@ def test_a_stream_that_is_behind():
     assert behind, "the stream was not behind: nothing was tested"
     for a, b in zip(got, want):
         assert same_bits(a, b)
+
+
+def test_the_widest_rows():
+    """2^24 elements a row, and one element less: every operator. Ones and zeros:
+    sums below 2^24, exact."""
+    dev = need_gpu()
+    g = gen(dev, 3)
+    for w in (2**24, 2**24 - 1):
+        table = torch.randint(0, 2, (5, w), generator=g, device=dev).to(BF16)
+        ids = torch.tensor([4, 0, -1, 4, 2], device=dev)
+        out = sdm().embedding(table, ids, 3.0)
+        for t, i in enumerate(ids.tolist()):
+            assert torch.equal(out[t], table[i] * 3 if i >= 0 else torch.zeros_like(out[t]))
+        same = torch.full((150,), 2, device=dev)  # three segments, joined
+        grad = sdm().embedding_grad(table[:1].expand(150, w), same, 3, dtype=F32)
+        assert torch.equal(grad[2], table[0].float() * 150) and not grad[:2].any()
+        pos = torch.tensor([[1, 3], [~4, 0], [2, ~5]], dtype=torch.int32, device=dev)
+        rows = sdm().dispatch(table[:3], pos)
+        for row, want in enumerate((table[1], table[0], table[2], table[0], None, None)):
+            assert torch.equal(rows[row], torch.zeros_like(table[0]) if want is None else want)
+        weights = torch.tensor([[2.0, 3], [5, 7], [1, 4]], device=dev)
+        out = sdm().combine(rows, pos, weights)
+        for t, s in enumerate((5, 7, 1)):
+            assert torch.equal(out[t], table[t] * s)
+        dout = table[2:]
+        grad_rows, grad_weights = sdm().combine_grad(dout, rows, pos, weights)
+        for (t, k), p in ((x, int(pos[x])) for x in ((0, 0), (0, 1), (1, 1), (2, 0))):
+            assert torch.equal(grad_rows[p], dout[t] * weights[t, k].to(BF16))
+            dot = (dout[t].float() * table[t].float()).sum(dtype=F64)
+            assert float(grad_weights[t, k]) == float(dot)
+        assert not grad_rows[4:].any() and grad_weights[1, 0] == 0 and grad_weights[2, 1] == 0
+
+
+def test_row_strides_past_2_31_elements():
+    dev = need_gpu()
+    ld, w = 2**31 + 5, 37
+    buf = torch.full((2 * ld + w,), 7.0, dtype=BF16, device=dev)
+    far = buf.as_strided((3, w), (ld, 1))
+    x = ints((3, w), 4, BF16, gen(dev, 9))
+    ids = torch.tensor([2, 0, 1], device=dev)
+    pos = ids.int()[:, None]
+    w2 = torch.full((3, 1), 2.0, device=dev)
+    back = torch.argsort(ids)
+    for fn, want in ((lambda a, o: sdm().embedding(a, ids, out=o), x[ids]),
+                     (lambda a, o: sdm().embedding_grad(a, ids, 3, out=o), x[back]),
+                     (lambda a, o: sdm().dispatch(a, pos, out=o), x[back]),
+                     (lambda a, o: sdm().combine(a, pos, w2, out=o), 2 * x[ids]),
+                     (lambda a, o: sdm().dispatch_grad(a, pos, out=o), x[ids]),
+                     (lambda a, o: sdm().combine_grad(a, a, pos, w2, out=o)[0], 2 * x[back])):
+        far.fill_(7.0)
+        assert torch.equal(fn(x, far), want)
+        far.copy_(x)
+        assert torch.equal(fn(far, None), want)
+    far.fill_(7.0)
+    for a in range(0, buf.numel(), 2**30):
+        assert bool((buf[a:a + 2**30] == 7.0).all())
+
+
+def test_the_longest_lookup():
+    """2^31 - 1 tokens of one element, two launches."""
+    dev = need_gpu()
+    n = 2**31 - 1
+    table = (torch.arange(100, device=dev) + 1).to(F16)[:, None]
+    ids = torch.empty(n, dtype=torch.int32, device=dev)
+    pieces = [(a, min(a + 2**28, n)) for a in range(0, n, 2**28)]
+    for a, b in pieces:
+        ids[a:b] = torch.arange(a, b, device=dev) % 101  # 100 is outside
+    out = sdm().embedding(table, ids)
+    for a, b in pieces:
+        want = torch.where(ids[a:b] < 100, ids[a:b] + 1, 0).to(F16)
+        assert torch.equal(out[a:b, 0], want), a
+
+
+def test_the_longest_list_of_the_gradient():
+    """2^30 tokens of one element: two sort passes of 256 tiles, 2^24 segments,
+    their partial rows folded. Ones and zeros, at most 1.2e6 of a row: exact."""
+    dev = need_gpu()
+    n, v = 2**30, 5000
+    ids = torch.empty(n, dtype=torch.int32, device=dev)
+    dout = torch.empty((n, 1), dtype=BF16, device=dev)
+    want = torch.zeros(v, dtype=torch.int64, device=dev)
+    for a in range(0, n, 2**27):
+        i = torch.arange(a, a + 2**27, device=dev)
+        some = (i * 2654435761) % 1_000_003
+        # a fifth of the tokens outside, row 4,999 several times the others
+        part = torch.where(some < 800_000, some % v, v)
+        part = torch.where(some % 1000 == 7, v - 1, part)
+        on = (i // 3) % 2
+        ids[a:a + 2**27], dout[a:a + 2**27, 0] = part.int(), on.to(BF16)
+        want += torch.bincount(part[on == 1], minlength=v + 1)[:v]
+    assert int(want.max()) < 2**24
+    grad = sdm().embedding_grad(dout, ids, v, dtype=F32)
+    assert torch.equal(grad[:, 0], want.float())
+
+
+@pytest.mark.parametrize("t,k,e", [(2**31 - 1, 1, 61), (238_000_000, 9, 4096)])
+def test_the_longest_routing(t, k, e):
+    """2^31 - 1 slots, and 2.142e9 over the most experts: the order is sorted, stable
+    and a permutation, position its inverse, and offsets where the experts start."""
+    dev = need_gpu()
+    n = t * k
+    experts = torch.empty(n, dtype=torch.int32, device=dev)
+    pieces = [(a, min(a + 2**27, n)) for a in range(0, n, 2**27)]
+    counts = torch.zeros(e + 1, dtype=torch.int64, device=dev)
+    for a, b in pieces:
+        i = torch.arange(a, b, device=dev)
+        experts[a:b] = ((i * 2654435761) % 1_000_003 % (e + 3)).int() - 1  # -1, e, e + 1: outside
+        x = experts[a:b]
+        counts += torch.bincount(torch.where((x >= 0) & (x < e), x, e), minlength=e + 1)
+    order, position, offsets = sdm().route(experts.reshape(t, k), e)
+    want = torch.cat([torch.zeros(1, dtype=torch.int64, device=dev), counts[:e].cumsum(0)])
+    assert torch.equal(offsets.long(), want)
+    position = position.reshape(-1)
+    last = torch.full((2,), -1, dtype=torch.int64, device=dev)  # the piece before's last key, slot
+    for a, b in pieces:
+        slot = order[a:b].long()
+        assert int(slot.min()) >= 0 and int(slot.max()) < n
+        x = experts[slot]
+        live = (x >= 0) & (x < e)
+        key = torch.where(live, x, e).long()
+        row = torch.arange(a, b, device=dev)
+        assert torch.equal(position[slot].long(), torch.where(live, row, ~row))
+        key, slot = torch.cat([last[:1], key]), torch.cat([last[1:], slot])
+        assert bool(((key[1:] > key[:-1]) | ((key[1:] == key[:-1]) & (slot[1:] > slot[:-1]))).all())
+        last = torch.stack([key[-1], slot[-1]])
+
+
+@pytest.mark.parametrize("n,v", [(70_000, 50_021), (300_001, 400), (300_001, 5_000_000)])
+def test_captured_gradient_of_long_lists(n, v):
+    """The sort by digits, the fold and the join in a graph, replayed on new tokens
+    between eager calls: the eager bits, accumulated ones too."""
+    dev = need_gpu()
+    g = gen(dev, n)
+    w = 12
+    ids = torch.zeros(n, dtype=torch.int64, device=dev)
+    dout = torch.zeros((n, w), dtype=BF16, device=dev)
+    total = torch.zeros((v, w), device=dev)
+
+    def fresh():
+        u = torch.rand(n, generator=g, device=dev, dtype=F64)
+        ids.copy_((u**6 * (v + 3)).long() - 1)  # row 0 and its neighbours often, some outside
+        dout.copy_(torch.randn((n, w), generator=g, device=dev))
+
+    def step(out):
+        grad = sdm().embedding_grad(dout, ids, v, 0.5)
+        sdm().embedding_grad(dout, ids, v, 0.5, out=out, accumulate=True)
+        return grad
+
+    fresh()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(total)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(total)
+    for _ in range(4):
+        fresh()
+        eager = total.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(captured, step(eager)) and same_bits(total, eager)
