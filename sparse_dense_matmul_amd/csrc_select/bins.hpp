@@ -10,13 +10,16 @@
 //    contiguous piece of the tile and counters of its own, so ranking needs no
 //    barrier between rounds: a round's 64 lanes rank equal digits by ballots,
 //    in lane order. A list of one tile needs no k_bin_count. Bound by latency:
-//    4.3 us in one launch at 512 slots over 128 experts, 4.9 + 9.9 us at 131,072.
-//  - k_rank: every element's place counted directly, one launch. Bound by integer
-//    issue: 5 us at 1,024 elements, 7 at 4,096, 11 at 8,192 (21 at 12,289).
+//    4.2 us in one launch at 512 slots over 128 experts, 11 at 4,096, 5.4 + 10.5
+//    us at 131,072, 4 + 19 at 524,288 over 256.
+//  - k_rank: every element's place counted directly, one launch: 3.8 us at 64
+//    elements and 4.4 at 1,024, a launch and two dependent reads; 7.0 at 4,096 and
+//    11.4 at 8,192, of which the compares' issue (below) explains 3.4.
 //  - k_chunk_rank / k_merge_rank: chunks of 1,024 placed directly, then every
 //    element's place found by binary searches in the other chunks, two launches:
-//    4 + 4 us at 12,289 elements (two passes by digits 28, in four launches),
-//    15 for the second at 65,536, bound by LDS reads.
+//    6.7 + 4.4 us at 12,289 elements, 11.9 + 14.8 at 65,536, the second bound by
+//    LDS reads.
+// Times are the kernels' own, in a trace, without the zeroing beside them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -160,7 +163,9 @@ k_bin_place(BinPass<I> ps, int bits, const int *__restrict__ counts, Out out,
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int nb = gridDim.x, blk = blockIdx.x, bins = ps.bins;
     // a piece is walked 4 rounds of 64 at a time, their loads issued together;
-    // the first four rounds' keys (all of a short list's) stay in registers
+    // the first four rounds' keys (all of a short list's) are loaded once. The
+    // choice between the two arrays in the counting loop puts them in scratch
+    // memory (48 bytes a lane), not in registers.
     const int64_t lo = (int64_t(blk) * kBinWaves + wave) * ps.piece;
     const int64_t hi = lo + ps.piece < ps.n ? lo + ps.piece : ps.n;
     uint32_t first_keys[4];
@@ -257,11 +262,16 @@ k_bin_place(BinPass<I> ps, int bits, const int *__restrict__ counts, Out out,
 // equal ones before it. A block holds all keys in LDS and places kRankTile
 // elements: a lane holds kRankHeld of them, so that a quad of keys read from
 // LDS serves four, and the block's lanes share the keys out between them. Two
-// integer operations a pair: over the card's 16,384 lanes n^2 / 8,192 cycles.
+// integer operations a pair: over the card's 16,384 lanes n^2 / 8,192 cycles, 0.05
+// us at 1,024 elements and 3.4 at 8,192. What else the time grows by there (every
+// block reads the whole list, and one block fills a CU) was not measured apart.
+// kRankMax: the whole gradient of width 8 takes 17.5 us so at 4,096 elements, 19.4
+// at 6,144, 21.6 at 8,192 and 29.2 at 10,240; by chunks and their merge 19.7, 20.1,
+// 20.8 and 21.5.
 constexpr int kRankThreads = 1024;
 constexpr int kRankHeld = 4;
 constexpr int kRankTile = 32;
-constexpr int kRankMax = 8192;   // most elements: above, k_merge_rank is as fast
+constexpr int kRankMax = 8192;   // most elements
 
 // The held elements' places among keys[0, padded) (in LDS, padded with ~0 to
 // whole quads), `first` the index of the block's first element there; left in
@@ -361,8 +371,11 @@ k_chunk_rank(const I *__restrict__ ids, int n, int64_t limit, int n_blocks, Plac
 // element's chunks and search several at once.
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeStage = 16;
-constexpr int kMergeMax = 65536;  // most elements: a pass over as many tokens takes 42 us,
-                                  // by digits 44; over twice as many 74 and 51
+// Most elements. The whole gradient of width 8 over a table of 50,021 rows takes 41
+// us so at 49,152 elements, 49.6 at 65,536 and 69 at 98,304; by digits, two passes,
+// 45, 49.4 and 53. Over 400 rows, one pass, the digits are ahead from 32,768 on: 27
+// for 29.5, at 65,536 32 for 45; the limit does not look at the table.
+constexpr int kMergeMax = 65536;
 
 constexpr size_t kMergeLds = size_t(kMergeStage * kChunkKeys) * 4;  // 64 KB
 

@@ -61,9 +61,9 @@ struct Chunks {
 };
 
 // out[t] = scale * table[ids[t]], or zeros for an id outside the table. Bound by
-// memory: the distinct rows read and the output written, 178 MB for 16,384
-// tokens of 4,096 bf16 in 33 us (5.4 TB/s; a large copy reaches 4.9). One step's
-// 32 tokens take 2.5 us, a launch and two dependent loads.
+// memory: 57 MB of distinct rows read and 134 written for 16,384 tokens of 4,096
+// bf16 in 34 us, 5.6 TB/s (a plain kernel that reads one byte for two written
+// reaches 6.0). One step's 32 tokens take 2.7 us, a launch and two dependent loads.
 template <typename T, typename I, int C, int U>
 __global__ void __launch_bounds__(kThreads)
 k_embed(const T *__restrict__ table, int64_t ld_table, int64_t n_rows, const I *__restrict__ ids,
@@ -204,8 +204,11 @@ __device__ __forceinline__ A wave_totals(A (&a)[N], int lane) {
 // slot's row and weight gradient are zero. W waves share a token's width, up to
 // eight of its slots at a time, so dout is read and rows and grad_rows are
 // streamed once; the dots' lane sums are added over the wave, then wave by wave:
-// a fixed order. Bound by memory: 131,072 rows of 2,048 bf16, 1.14 GB, in 208 us
-// (5.5 TB/s, half of it written).
+// a fixed order. Bound by memory: 131,072 rows of 2,048 bf16, 1.14 GB, in 209 us
+// (5.5 TB/s, half of it written). Rows of fewer than 64 chunks leave lanes idle: as
+// many rows of 128 bf16 take 28 us, 71 MB at 2.5 TB/s. float64 goes through 80 bytes
+// of scratch a lane (wave_totals' choice between array elements): 131,072 rows of
+// 512, 1.14 GB, 216 us.
 template <typename T, int C, int W, bool ONCE>
 __global__ void __launch_bounds__(kThreads)
 k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict__ rows,
@@ -282,9 +285,9 @@ k_combine_grad(const T *__restrict__ dout, int64_t ld_dout, const T *__restrict_
         }
         __syncthreads();
     };
-    // one batch for five to seven slots, not two or three: each has a round of
-    // loads and two barriers of its own (six slots of 1,001 f32 54 -> 47 us with the
-    // gradient of the dispatch; the combine, without barriers, gains nothing so)
+    // one batch for three or five to seven slots, not two or three: each has a round
+    // of loads and two barriers of its own (3,001 tokens of six slots of 1,001 f32 37
+    // -> 30 us, of three 18.6 -> 16.3; the combine, without barriers, gains nothing so)
     by_padded_eights(top_k, batch);
 }
 
@@ -387,8 +390,9 @@ GradPlan grad_plan(int elt, int64_t width, int64_t n) {
     g.cpr = (width + g.chunk - 1) / g.chunk;
     // narrow rows: four groups of 16 lanes a wave, and so segments of at most 16; in
     // long lists a group of 64, most of its lanes idle, for segments of 64 (1,000,000
-    // tokens of 64 bf16 over 32,000 ids 410 -> 134 us, of one id 111 -> 137; 65,536
-    // 40 and 40, of one id 42 -> 79)
+    // tokens of 64 bf16 over 32,000 ids 410 -> 134 us, but of one id 111 -> 137). At
+    // the border itself the groups of 16 are still ahead: 131,071 tokens 43.5 us and
+    // 131,072 49.8, Zipf's ids 54 and 60, of one id 49 and 92.
     g.lanes = g.cpr > 16 || n >= 1 << 17 ? 64 : 16;
     g.slices = int((g.cpr + g.lanes - 1) / g.lanes);
     // 2,048 groups or more as far as segments of 4 go: shorter segments leave more

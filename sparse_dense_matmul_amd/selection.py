@@ -35,7 +35,7 @@ def _public_raw_stream(index):
 
 
 # the current stream's handle without the Stream object around it: 0.1 us where
-# the public way takes 2, of a 10 us call. A torch without this private function
+# the public way takes 2, of a 7 us call. A torch without this private function
 # takes the public way; importing the package needs neither.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
