@@ -523,7 +523,8 @@ typedef enum {
     VSPMM_ELT_F32 = 0,
     VSPMM_ELT_F64 = 1,
     VSPMM_ELT_BF16 = 2,
-    VSPMM_ELT_F16 = 3
+    VSPMM_ELT_F16 = 3,
+    VSPMM_ELT_MX4 = 4 /* microscaled 4-bit: the weights of vspmm_expert_mlp only */
 } vspmm_elt;
 typedef enum { VSPMM_INDEX_I32 = 0, VSPMM_INDEX_I64 = 1 } vspmm_index;
 
@@ -604,6 +605,98 @@ vspmm_status vspmm_combine_grad(vspmm_elt elt, int64_t n_tokens, int64_t top_k, 
                                 int64_t ld_rows, const int32_t *position, const void *weight,
                                 void *grad_rows, int64_t ld_grad_rows, void *grad_weight,
                                 hipStream_t stream);
+
+/* Microscaled 4-bit matrices: the compressed layout of a language model's
+ * weights and activations. A value is a 4-bit code (bit 3 the sign, bits 0 .. 2
+ * one of 0, 0.5, 1, 1.5, 2, 3, 4, 6) times the scale 2^(b - 127) of its block of
+ * 32 values of a row, b one byte; b = 255 makes the block NaN. Row r holds
+ * 16 * blocks bytes of codes from codes + r * ld_codes, blocks = ceil(width /
+ * 32), value 2 j in the low half of byte j, and blocks bytes of scales from
+ * scales + r * ld_scales. Codes past the width are zero. Strides are in bytes,
+ * >= 0; any alignment is served. The matrix is never expanded in memory: the
+ * products widen codes in registers, or feed them to the matrix cores.
+ *
+ * Conventions of these calls are those of the selection products. Dense
+ * operands are VSPMM_ELT_BF16 or _F16 (also _F32 where said). Every product
+ * multiplies its operands' exact values and sums in float32, in an order that
+ * depends only on the sizes and types; results are rounded once. A value past
+ * float32's (a scale byte above 252) counts as infinite. Extents of rows are at
+ * most 2^30, widths at most 2^24 (_UNSUPPORTED above). */
+typedef struct {
+    const uint8_t *codes;  /* device */
+    const uint8_t *scales; /* device */
+    int64_t ld_codes, ld_scales;
+} vspmm_mx4;
+
+/* The rows of x (transpose == 0: rows x width), or of its transpose (width x
+ * rows; the layout of a product that contracts x's rows, as the gradient of
+ * weights does), to contiguous codes (n x 16 * blocks bytes) and scales (n x
+ * blocks bytes). A block's scale has the exponent of its largest magnitude less
+ * 2, at least 2^-127; a value over its scale is rounded to the nearest code, ties
+ * to even, past 6 to 6. A block with an infinity or NaN becomes NaN. elt: _F32,
+ * _BF16 or _F16. Errors: _NULL, _DIM, _ENUM, _UNSUPPORTED, _HIP. */
+vspmm_status vspmm_mx4_quantize(vspmm_elt elt, int32_t transpose, int64_t rows, int64_t width,
+                                const void *x, int64_t ld_x, uint8_t *codes, uint8_t *scales,
+                                hipStream_t stream);
+
+/* out[r] = the values of x's row r, rounded to elt (_F32, _BF16 or _F16).
+ * Errors: as vspmm_mx4_quantize. */
+vspmm_status vspmm_mx4_dequantize(vspmm_elt elt, int64_t rows, int64_t width, const vspmm_mx4 *x,
+                                  void *out, int64_t ld_out, hipStream_t stream);
+
+/* out (m x n) = x (m x width, dense) times the transpose of w (n x width). x and
+ * out are of elt. Errors: as vspmm_mx4_quantize. */
+vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width, const void *x,
+                              int64_t ld_x, const vspmm_mx4 *w, void *out, int64_t ld_out,
+                              hipStream_t stream);
+
+/* The gradient of vspmm_mx4_matmul with respect to x: grad (m x width) = dout (m
+ * x n) times w. Errors: as vspmm_mx4_quantize. */
+vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t width,
+                                   const void *dout, int64_t ld_dout, const vspmm_mx4 *w,
+                                   void *grad, int64_t ld_grad, hipStream_t stream);
+
+/* out (m x n, of elt: _F32, _BF16 or _F16) = x (m x width) times the transpose of
+ * w (n x width), both in 4 bits. Errors: as vspmm_mx4_quantize. */
+vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t width,
+                                  const vspmm_mx4 *x, const vspmm_mx4 *w, void *out,
+                                  int64_t ld_out, hipStream_t stream);
+
+/* One matrix (rows x columns) of every expert: expert e's row r starts at data +
+ * e * stride + r * ld, in elements of a 16-bit type, or in bytes of codes with
+ * its scales at scales + e * stride_scales + r * ld_scales. */
+typedef struct {
+    const void *data;      /* device */
+    int64_t ld, stride;
+    const uint8_t *scales; /* device; 4-bit weights only */
+    int64_t ld_scales, stride_scales;
+} vspmm_expert_matrix;
+typedef enum { VSPMM_SILU = 0, VSPMM_GELU = 1 } vspmm_activation;
+
+/* A whole mixture-of-experts layer for a few tokens (up to 1,024), in two
+ * launches: with e = experts[t, k],
+ *   out[t] = sum over k of weight[t, k] * down_e (act(gate_e x[t]) * (up_e x[t])).
+ * gate and up: hidden x width, down: width x hidden, of weights_elt: elt itself
+ * or VSPMM_ELT_MX4. experts: device int32 or int64 [n_tokens, top_k]; a choice
+ * outside [0, n_experts) adds nothing, and only the weights of experts that some
+ * token chose are read. weight: device float32 [n_tokens, top_k]. act: x / (1 +
+ * exp(-x)), or x / 2 (1 + erf(x / sqrt 2)). Sums and activations are in float32;
+ * a hidden value is held to 17 bits. A token's result does not depend on the
+ * others' values. More tokens: vspmm_route, vspmm_dispatch, a product per expert
+ * and vspmm_combine. ws: vspmm_expert_mlp_workspace_size bytes. Errors: _NULL,
+ * _DIM, _ENUM, _WORKSPACE, _UNSUPPORTED (more than 1,024 tokens, 4,096 experts or
+ * choices a token, or rows of more than 2^24), _HIP. */
+vspmm_status vspmm_expert_mlp(vspmm_elt elt, vspmm_elt weights_elt, vspmm_index index,
+                              vspmm_activation activation, int64_t n_tokens, int64_t top_k,
+                              int64_t n_experts, int64_t width, int64_t hidden, const void *x,
+                              int64_t ld_x, const void *experts, const float *weight,
+                              const vspmm_expert_matrix *gate, const vspmm_expert_matrix *up,
+                              const vspmm_expert_matrix *down, void *out, int64_t ld_out, void *ws,
+                              size_t ws_bytes, hipStream_t stream);
+/* Workspace bytes of vspmm_expert_mlp. bytes: host. Errors: _NULL, _DIM,
+ * _UNSUPPORTED. */
+vspmm_status vspmm_expert_mlp_workspace_size(int64_t n_tokens, int64_t top_k, int64_t n_experts,
+                                             int64_t width, int64_t hidden, size_t *bytes);
 
 /* A static string naming the status. */
 const char *vspmm_status_string(vspmm_status st);

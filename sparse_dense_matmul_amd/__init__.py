@@ -12,8 +12,9 @@ raises ImportError, and a call that the library rejects raises VspmmError.
     A.T                  # the transpose, a VCSC over the same arrays
 
 Products with a selection matrix (embedding lookup, tokens routed to experts
-and back, their gradients) are in :mod:`sparse_dense_matmul_amd.selection` and
-offered here too.
+and back, their gradients) are in :mod:`sparse_dense_matmul_amd.selection`,
+microscaled 4-bit matrices and the experts' layer in
+:mod:`sparse_dense_matmul_amd.mx4`; both are offered here too.
 """
 
 from __future__ import annotations
@@ -23,9 +24,10 @@ import os
 
 import torch
 
-__all__ = ["VcsMatrix", "CsrMatrix", "Schedule", "VspmmError", "assemble_csr", "Routing",
-           "combine", "combine_grad", "dispatch", "dispatch_grad", "embedding", "embedding_grad",
-           "embedding_grad_workspace", "route", "lib", "LIB_PATH", "EXPORTS"]
+__all__ = ["VcsMatrix", "CsrMatrix", "Schedule", "VspmmError", "assemble_csr", "Mx4", "Routing",
+           "combine", "combine_grad", "dequantize_mx4", "dispatch", "dispatch_grad", "embedding",
+           "embedding_grad", "embedding_grad_workspace", "expert_mlp", "expert_mlp_workspace",
+           "matmul_mx4", "matmul_mx4_grad", "quantize_mx4", "route", "lib", "LIB_PATH", "EXPORTS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvspmm.so")
@@ -86,6 +88,15 @@ EXPORTS = {
                       ctypes.c_int),
     "vspmm_combine_grad": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64,
                             _vp, _vp], ctypes.c_int),
+    "vspmm_mx4_quantize": ([_i32, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp], ctypes.c_int),
+    "vspmm_mx4_dequantize": ([_i32, _i64, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "vspmm_mx4_matmul": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "vspmm_mx4_matmul_grad": ([_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp],
+                              ctypes.c_int),
+    "vspmm_mx4_matmul_mx4": ([_i32, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp], ctypes.c_int),
+    "vspmm_expert_mlp": ([_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp,
+                          _vp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp], ctypes.c_int),
+    "vspmm_expert_mlp_workspace_size": ([_i64, _i64, _i64, _i64, _i64, _P(_sz)], ctypes.c_int),
     "vspmm_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "vspmm_set_view": ([_vp, _i32, _vp, _vp, _i64], ctypes.c_int),
     "vspmm_view_name": ([_i32], ctypes.c_char_p),
@@ -612,3 +623,5 @@ def assemble_csr(role: str, n_out: int, n_in: int, elem_ptr, out_idx, in_idx, we
 
 from .selection import (Routing, combine, combine_grad, dispatch, dispatch_grad,  # noqa: E402
                         embedding, embedding_grad, embedding_grad_workspace, route)
+from .mx4 import (Mx4, dequantize_mx4, expert_mlp, expert_mlp_workspace,  # noqa: E402
+                  matmul_mx4, matmul_mx4_grad, quantize_mx4)

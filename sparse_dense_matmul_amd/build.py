@@ -3,7 +3,8 @@
 Run as ``python -m sparse_dense_matmul_amd.build`` or through
 ``__graft_entry__.build()``. The library lands next to this file, where the
 binding loads it from. Each translation unit (the host code with the layout
-builders, one per kernel family and the selection products; the VCS walks once
+builders, one per kernel family, the selection products, the 4-bit products and the
+experts' layer; the VCS walks once
 per vector width and k_short once per element type) is
 compiled to an object in parallel under ``_build/``, then the objects are
 linked into the library.
@@ -22,6 +23,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 # the selection products (embedding, routing), beside the walks' sources
 SELECT = os.path.join("..", "csrc_select", "select.hip")
+# microscaled 4-bit matrices and the experts' layer
+MX4 = os.path.join("..", "csrc_mx4", "product.hip")
+EXPERTS = os.path.join("..", "csrc_mx4", "experts.hip")
 LIB = os.path.join(HERE, "libvspmm.so")
 # the benchmark's ceiling probes (not part of the product library)
 PROBE_LIB = os.path.join(HERE, "libvspmm_probe.so")
@@ -36,6 +40,8 @@ UNITS = [
     ("walk_plain.hip", [], "walk_plain"),
     ("walk_scatter.hip", [], "walk_scatter"),
     (SELECT, [], "select"),
+    (MX4, [], "mx4"),
+    (EXPERTS, [], "experts"),
 ] + [(f"walk_vcs_{kind}.hip", [f"-DVSPMM_VEC={v}"], f"walk_vcs_{kind}_v{v}")
      for kind in ("rows", "long") for v in (1, 2, 4)]
 ARCH = "gfx950"

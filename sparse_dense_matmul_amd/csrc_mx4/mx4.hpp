@@ -1,0 +1,117 @@
+// Microscaled 4-bit matrices: codes of 4 bits (sign, two exponent bits, one mantissa bit), 32 to a 16-byte block of a
+// row with value 2 j in the low half of byte j, and one power of two 2^(b - 127) a block (b = 255: not a number).
+// gfx950 converts between the codes and 16- or 32-bit floats with the scale applied (v_cvt_scalef32_pk_*; the scale
+// operand's exponent field is the byte b) and multiplies them in its matrix instructions. Both were checked here for
+// every code and scale: values are exact where the type holds them, b = 255 gives NaN, conversions to codes round to
+// nearest even and saturate, and the matrix instructions keep subnormal operands and results.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../csrc_select/rows.hpp"
+
+namespace vspmm {
+
+constexpr int kBlock = 32;       // values of a block
+constexpr int kBlockBytes = 16;  // their codes
+
+using i32x4 = int32_t __attribute__((ext_vector_type(4)));
+using i32x8 = int32_t __attribute__((ext_vector_type(8)));
+using f32x2 = float __attribute__((ext_vector_type(2)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using f32x16 = float __attribute__((ext_vector_type(16)));
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
+
+// 16 bytes at the alignment of one element of 16 bits, or of a byte.
+using Half16 = i32x4 __attribute__((aligned(2)));
+using Byte16 = i32x4 __attribute__((aligned(1)));
+
+struct Mx4 {};     // element type of a microscaled matrix
+struct Planes {};  // float32 values as the sum of two bfloat16 ones, each in an array of its own
+
+template <typename T, typename F>
+__device__ __forceinline__ T bits_as(F x) {
+    static_assert(sizeof(T) == sizeof(F));
+    return __builtin_bit_cast(T, x);
+}
+
+// The scale operand of the conversions.
+__device__ __forceinline__ float scale_operand(uint32_t b) { return __uint_as_float(b << 23); }
+
+// Eight codes (a word) as eight values of 16 bits.
+template <typename T>
+__device__ __forceinline__ i32x4 widen(uint32_t codes, float scale) {
+    i32x4 r;
+    if constexpr (std::is_same_v<T, bf16>) {
+        r[0] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
+        r[1] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1));
+        r[2] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
+        r[3] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
+    } else {
+        r[0] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0));
+        r[1] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1));
+        r[2] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2));
+        r[3] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3));
+    }
+    return r;
+}
+
+// Whether float16 holds every value of a block of this scale exactly: 0.5 * 2^-23 is its least subnormal and
+// 6 * 2^13 lies below its largest number.
+__device__ __forceinline__ bool f16_scale(uint32_t b) { return b - 104u <= 36u; }
+
+// Eight float16 values as the sum of two bfloat16 each: the upper eight bits of the significand, and the rest, which
+// has at most three. Exact: float16's least subnormal is a normal bfloat16. An infinity or NaN goes into the first.
+__device__ __forceinline__ void split(i32x4 v, i32x4 &hi, i32x4 &lo) {
+    const f16x8 x = bits_as<f16x8>(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = float(x[2 * i]), b = float(x[2 * i + 1]);
+        const uint32_t ua = __float_as_uint(a) & 0xffff0000u, ub = __float_as_uint(b) & 0xffff0000u;
+        hi[i] = int32_t((ua >> 16) | ub);
+        // x - x for an infinity: its second part is zero
+        const float la = __builtin_isinf(a) ? 0.0f : a - __uint_as_float(ua);
+        const float lb = __builtin_isinf(b) ? 0.0f : b - __uint_as_float(ub);
+        lo[i] = int32_t((__float_as_uint(la) >> 16) | (__float_as_uint(lb) & 0xffff0000u));
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ f32x4 mma16(i32x4 a, i32x4 b, f32x4 c) {
+    if constexpr (std::is_same_v<T, bf16>)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(bits_as<bf16x8>(a), bits_as<bf16x8>(b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(bits_as<f16x8>(a), bits_as<f16x8>(b), c, 0, 0, 0);
+}
+
+template <typename T>
+__device__ __forceinline__ f32x16 mma32(i32x4 a, i32x4 b, f32x16 c) {
+    if constexpr (std::is_same_v<T, bf16>)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(bits_as<bf16x8>(a), bits_as<bf16x8>(b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(bits_as<f16x8>(a), bits_as<f16x8>(b), c, 0, 0, 0);
+}
+
+// The product of two blocks of 4-bit codes, each with its scales in byte I of a word.
+template <int I>
+__device__ __forceinline__ f32x4 mma16_mx4(i32x4 a, uint32_t sa, i32x4 b, uint32_t sb, f32x4 c) {
+    const i32x8 a8 = __builtin_shufflevector(a, i32x4{}, 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 b8 = __builtin_shufflevector(b, i32x4{}, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, I, int(sa), I, int(sb));
+}
+template <int I>
+__device__ __forceinline__ f32x16 mma32_mx4(i32x4 a, uint32_t sa, i32x4 b, uint32_t sb, f32x16 c) {
+    const i32x8 a8 = __builtin_shufflevector(a, i32x4{}, 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 b8 = __builtin_shufflevector(b, i32x4{}, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, I, int(sa), I, int(sb));
+}
+
+__host__ __device__ constexpr int64_t blocks_of_width(int64_t width) { return (width + kBlock - 1) / kBlock; }
+
+}  // namespace vspmm

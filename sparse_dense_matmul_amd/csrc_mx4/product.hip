@@ -1,0 +1,272 @@
+// Microscaled 4-bit matrices: quantisation and back, products with dense and with 4-bit tokens, and the gradient of
+// the tokens. Declared in include/vspmm.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "few.hpp"
+#include "host.hpp"
+#include "quantize.hpp"
+#include "tile.hpp"
+
+using namespace vspmm;
+
+namespace {
+
+// ------------------------------------------------------------------ kernels
+
+// Eight waves share 16 R rows and 16 MT tokens, each over an eighth of the contraction; their sums meet in LDS.
+constexpr int kFewWaves = 8;
+template <typename X, typename O, int R, int MT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_few(Row<X> x, int64_t ld_x, int64_t ld_xs, Row<Mx4> w,
+                                                        int64_t ld_codes, int64_t ld_scales, O *__restrict__ out,
+                                                        int64_t ld_out, int m, int n, int k) {
+    __shared__ f32x4 parts[kFewWaves][R][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, g = lane >> 4;
+    const int n0 = int(blockIdx.x) * 16 * R, m0 = int(blockIdx.y) * 16 * MT;
+    Row<Mx4> rows[R];
+    Row<X> tokens[MT];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t row = min(n0 + 16 * i + r, n - 1);
+        rows[i] = {w.codes + row * ld_codes, w.scales + row * ld_scales};
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int64_t row = min(m0 + 16 * t + r, m - 1);
+        if constexpr (std::is_same_v<X, Mx4>) tokens[t] = {x.codes + row * ld_x, x.scales + row * ld_xs};
+        else tokens[t] = {x.p + row * ld_x};
+    }
+    const int chunks = (k + kChunkK - 1) / kChunkK;
+    f32x4 acc[R][MT] = {};
+    accumulate<(MT == 1 ? 4 : MT == 2 ? 2 : 1)>(acc, rows, tokens, chunks * wave / kFewWaves,
+                                                chunks * (wave + 1) / kFewWaves, k, g, ~0u);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        if (t) __syncthreads();
+#pragma unroll
+        for (int i = 0; i < R; ++i) parts[wave][i][lane] = acc[i][t];
+        __syncthreads();
+        if (int(threadIdx.x) < 64 * R) {
+            f32x4 sum = parts[0][wave][lane];
+#pragma unroll
+            for (int v = 1; v < kFewWaves; ++v) sum += parts[v][wave][lane];
+            const int mm = m0 + 16 * t + r, nn = n0 + 16 * wave + 4 * g;
+            if (mm < m) {
+                Vec<O, 4> o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = rounded<O>(sum[e]);
+                O *at = out + mm * ld_out + nn;
+                if (nn + 4 <= n) {
+                    store_vec<4>(at, o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (nn + e < n) at[e] = o[e];
+                }
+            }
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void k_zero_rows(ZeroRows z) { z.run(0); }
+
+// --------------------------------------------------------------------- host
+
+template <typename O>
+vspmm_status zero_rows(O *out, int64_t ld, int64_t rows, int64_t width, hipStream_t s) {
+    const ZeroRows z(out, ld * int64_t(sizeof(O)), rows, width * int64_t(sizeof(O)));
+    hipLaunchKernelGGL(k_zero_rows, dim3(z.blocks(256)), dim3(256), 0, s, z);
+    return launched();
+}
+
+// Tiles of a product past one launch are of more than 2^43 results.
+bool too_many(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) / 64) > kI32Max; }
+
+// Up to this many tokens the few-token kernel, bound by the matrix's bytes; tiles beyond.
+constexpr int64_t kFewTokens = 64;
+
+template <typename X, typename O>
+void launch_few(Row<X> x, int64_t ld_x, int64_t ld_xs, const vspmm_mx4 &w, O *out, int64_t ld_out, int m, int n, int k,
+                hipStream_t s) {
+    const Row<Mx4> rows{w.codes, w.scales};
+    auto go = [&](auto r, auto mt) {
+        constexpr int R = decltype(r)::value, MT = decltype(mt)::value;
+        hipLaunchKernelGGL((k_few<X, O, R, MT>), dim3((n + 16 * R - 1) / (16 * R), (m + 16 * MT - 1) / (16 * MT)),
+                           dim3(64 * kFewWaves), 0, s, x, ld_x, ld_xs, rows, w.ld_codes, w.ld_scales, out, ld_out, m, n,
+                           k);
+    };
+    using std::integral_constant;
+    if (m <= 16) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    else if (m <= 32) go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    else go(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+}
+
+// The tile's edge / 64: the largest whose tiles occupy the 256 compute units.
+int tile_width(int64_t m, int64_t n) {
+    for (int tw = 4; tw > 1; tw /= 2)
+        if (((m + 64 * tw - 1) / (64 * tw)) * ((n + 64 * tw - 1) / (64 * tw)) >= 224) return tw;
+    return 1;
+}
+
+template <typename F>
+void with_tile(int64_t m, int64_t n, F &&f) {
+    switch (tile_width(m, n)) {
+        case 4: return f(std::integral_constant<int, 4>{});
+        case 2: return f(std::integral_constant<int, 2>{});
+        default: return f(std::integral_constant<int, 1>{});
+    }
+}
+
+TileShape tile_shape(int64_t m, int64_t n, int64_t k, int edge, unsigned &tiles) {
+    const int64_t tn = (n + edge - 1) / edge;
+    tiles = unsigned(((m + edge - 1) / edge) * tn);
+    return TileShape{int(m), int(n), int(k), uint32_t(tn)};
+}
+
+}  // namespace
+
+extern "C" {
+
+vspmm_status vspmm_mx4_quantize(vspmm_elt elt, int32_t transpose, int64_t rows, int64_t width, const void *x,
+                                int64_t ld_x, uint8_t *codes, uint8_t *scales, hipStream_t stream) {
+    if (!dense_elt(elt) && elt != VSPMM_ELT_F32) return VSPMM_ERR_ENUM;
+    if (vspmm_status st = check_dense(rows, width, ld_x, x)) return st;
+    if (transpose && rows > kWidthMax) return VSPMM_ERR_UNSUPPORTED;
+    const int64_t n = transpose ? width : rows, blocks = blocks_of_width(transpose ? rows : width);
+    if (n == 0 || blocks == 0) return VSPMM_OK;
+    if (!codes || !scales) return VSPMM_ERR_NULL;
+    auto run = [&](auto e) {
+        using T = decltype(e);
+        const T *p = static_cast<const T *>(x);
+        if (transpose) {
+            const int64_t col_tiles = (width + kTransposeCols - 1) / kTransposeCols;
+            const int64_t tiles = col_tiles * ((blocks + kTransposeWaves - 1) / kTransposeWaves);
+            if (tiles > kI32Max) return VSPMM_ERR_UNSUPPORTED;
+            hipLaunchKernelGGL(k_quantize_transposed<T>, dim3(unsigned(tiles)), dim3(64 * kTransposeWaves), 0, stream, p, ld_x,
+                               int(rows), int(width), int(blocks), uint32_t(col_tiles), codes, scales);
+            return launched();
+        }
+        const uint32_t per_row = uint32_t(4 * blocks);
+        const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per_row);
+        for (int64_t r = 0; r < rows; r += most) {
+            const uint32_t lanes = uint32_t(std::min(most, rows - r)) * per_row;
+            hipLaunchKernelGGL(k_quantize<T>, dim3((lanes + 255) / 256), dim3(256), 0, stream, p + r * ld_x, ld_x, lanes,
+                               FastDiv(per_row), per_row, int(width), codes + r * blocks * kBlockBytes,
+                               scales + r * blocks);
+        }
+        return launched();
+    };
+    return elt == VSPMM_ELT_F32 ? run(float{}) : with_dense(elt, run);
+}
+
+vspmm_status vspmm_mx4_dequantize(vspmm_elt elt, int64_t rows, int64_t width, const vspmm_mx4 *x, void *out,
+                                  int64_t ld_out, hipStream_t stream) {
+    if (!dense_elt(elt) && elt != VSPMM_ELT_F32) return VSPMM_ERR_ENUM;
+    if (vspmm_status st = check_mx4(x, rows, width)) return st;
+    if (vspmm_status st = check_written(rows, width, ld_out, out)) return st;
+    if (rows == 0 || width == 0) return VSPMM_OK;
+    auto run = [&](auto e) {
+        using T = decltype(e);
+        const uint32_t per_row = uint32_t(4 * blocks_of_width(width));
+        const int64_t most = std::max<int64_t>(1, (int64_t(1) << 30) / per_row);
+        for (int64_t r = 0; r < rows; r += most) {
+            const uint32_t lanes = uint32_t(std::min(most, rows - r)) * per_row;
+            hipLaunchKernelGGL(k_dequantize<T>, dim3((lanes + 255) / 256), dim3(256), 0, stream,
+                               x->codes + r * x->ld_codes, x->ld_codes, x->scales + r * x->ld_scales, x->ld_scales,
+                               lanes, FastDiv(per_row), per_row, int(width), static_cast<T *>(out) + r * ld_out, ld_out);
+        }
+        return launched();
+    };
+    return elt == VSPMM_ELT_F32 ? run(float{}) : with_dense(elt, run);
+}
+
+vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width, const void *x, int64_t ld_x,
+                              const vspmm_mx4 *w, void *out, int64_t ld_out, hipStream_t stream) {
+    if (!dense_elt(elt)) return VSPMM_ERR_ENUM;
+    if (vspmm_status st = check_dense(m, width, ld_x, x)) return st;
+    if (vspmm_status st = check_mx4(w, n, width)) return st;
+    if (vspmm_status st = check_written(m, n, ld_out, out)) return st;
+    if (m == 0 || n == 0) return VSPMM_OK;
+    if (too_many(m, n)) return VSPMM_ERR_UNSUPPORTED;
+    return with_dense(elt, [&](auto e) {
+        using T = decltype(e);
+        T *o = static_cast<T *>(out);
+        if (width == 0) return zero_rows(o, ld_out, m, n, stream);
+        if (m <= kFewTokens) {
+            launch_few(Row<T>{static_cast<const T *>(x)}, ld_x, 0, *w, o, ld_out, int(m), int(n), int(width), stream);
+            return launched();
+        }
+        with_tile(m, n, [&](auto tw) {
+            constexpr int TW = decltype(tw)::value;
+            unsigned tiles;
+            const TileShape s = tile_shape(m, n, width, 64 * TW, tiles);
+            allow_lds(reinterpret_cast<const void *>(&k_tile<TW, T, T>), tile_lds<TW>());
+            hipLaunchKernelGGL((k_tile<TW, T, T>), dim3(tiles), dim3(kTileThreads), tile_lds<TW>(), stream,
+                               static_cast<const T *>(x), ld_x, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
+                               ld_out, s);
+        });
+        return launched();
+    });
+}
+
+vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t width, const void *dout, int64_t ld_dout,
+                                   const vspmm_mx4 *w, void *grad, int64_t ld_grad, hipStream_t stream) {
+    if (!dense_elt(elt)) return VSPMM_ERR_ENUM;
+    if (vspmm_status st = check_dense(m, n, ld_dout, dout)) return st;
+    if (vspmm_status st = check_mx4(w, n, width)) return st;
+    if (vspmm_status st = check_written(m, width, ld_grad, grad)) return st;
+    if (m == 0 || width == 0) return VSPMM_OK;
+    if (too_many(m, width)) return VSPMM_ERR_UNSUPPORTED;
+    return with_dense(elt, [&](auto e) {
+        using T = decltype(e);
+        T *o = static_cast<T *>(grad);
+        if (n == 0) return zero_rows(o, ld_grad, m, width, stream);
+        with_tile(m, width, [&](auto tw) {
+            constexpr int TW = decltype(tw)::value;
+            unsigned tiles;
+            const TileShape s = tile_shape(m, width, n, 64 * TW, tiles);
+            allow_lds(reinterpret_cast<const void *>(&k_tile_grad<TW, T>), grad_lds<TW>());
+            hipLaunchKernelGGL((k_tile_grad<TW, T>), dim3(tiles), dim3(kTileThreads), grad_lds<TW>(), stream,
+                               static_cast<const T *>(dout), ld_dout, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
+                               ld_grad, s);
+        });
+        return launched();
+    });
+}
+
+vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t width, const vspmm_mx4 *x,
+                                  const vspmm_mx4 *w, void *out, int64_t ld_out, hipStream_t stream) {
+    if (!dense_elt(elt) && elt != VSPMM_ELT_F32) return VSPMM_ERR_ENUM;
+    if (vspmm_status st = check_mx4(x, m, width)) return st;
+    if (vspmm_status st = check_mx4(w, n, width)) return st;
+    if (vspmm_status st = check_written(m, n, ld_out, out)) return st;
+    if (m == 0 || n == 0) return VSPMM_OK;
+    if (too_many(m, n)) return VSPMM_ERR_UNSUPPORTED;
+    auto run = [&](auto e) {
+        using T = decltype(e);
+        T *o = static_cast<T *>(out);
+        if (width == 0) return zero_rows(o, ld_out, m, n, stream);
+        if (m <= kFewTokens) {
+            launch_few(Row<Mx4>{x->codes, x->scales}, x->ld_codes, x->ld_scales, *w, o, ld_out, int(m), int(n),
+                       int(width), stream);
+            return launched();
+        }
+        with_tile(m, n, [&](auto tw) {
+            constexpr int TW = decltype(tw)::value;
+            unsigned tiles;
+            const TileShape s = tile_shape(m, n, width, 64 * TW, tiles);
+            allow_lds(reinterpret_cast<const void *>(&k_tile_both<TW, T>), both_lds<TW>());
+            hipLaunchKernelGGL((k_tile_both<TW, T>), dim3(tiles), dim3(kTileThreads), both_lds<TW>(), stream, x->codes,
+                               x->ld_codes, x->scales, x->ld_scales, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
+                               ld_out, s);
+        });
+        return launched();
+    };
+    return elt == VSPMM_ELT_F32 ? run(float{}) : with_dense(elt, run);
+}
+
+}  // extern "C"
