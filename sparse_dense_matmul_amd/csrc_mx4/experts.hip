@@ -38,11 +38,16 @@ struct Choices {
     }
 };
 
-// Between the launches: how many experts are in use, which, each one's slot of each token (-1: not sent there; a token
-// sent twice to an expert has one, with both weights), and the hidden values by slot.
+// Between the launches: how many experts are in use, which, the tokens sent to each in order with a slot of each (a
+// token sent twice to an expert is listed once, with both weights), where the list passes each multiple of kGroup
+// tokens, and the hidden values by slot, in whole chunks with zeros at the end.
+constexpr int kGroup = 128, kGroups = kTokensMax / kGroup;
 struct Between {
-    int *count, *expert, *slot;  // [1], [most], [most, tokens]
-    bf16 *hi, *lo;               // [slots, hidden]
+    int *count, *expert;  // [1], [most]
+    int *bounds;          // [most, kGroups + 1]
+    int2 *list;           // [most, tokens]: token, slot
+    bf16 *hi, *lo;        // [slots, padded]
+    int64_t padded;
 };
 
 template <typename T>
@@ -129,7 +134,6 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
                 weight[i] = slot[i] < 0 ? ch.weights[s] : weight[i] + ch.weights[s];
                 if (slot[i] < 0) slot[i] = s;
             }
-            if (blockIdx.x == 0) to.slot[int64_t(a) * ch.tokens + t] = slot[i];
         }
         here[i] = __ballot(slot[i] >= 0);
         if (lane == 0) s_counts[i * kUpWaves + wave] = __popcll(here[i]);
@@ -141,35 +145,40 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
     for (int i = 0; i < GROUPS; ++i) {
         int at = 0;
         for (int c = 0; c < i * kUpWaves + wave; ++c) at += s_counts[c];
+        const int group = i * kUpWaves + wave;
+        if (blockIdx.x == 0 && lane == 0 && group % (kGroup / 64) == 0)
+            to.bounds[int64_t(a) * (kGroups + 1) + group / (kGroup / 64)] = at;
         if (slot[i] >= 0) {
             at += __popcll(here[i] & ((uint64_t(1) << lane) - 1));
-            s_token[at] = uint16_t((i * kUpWaves + wave) * 64 + lane);
+            s_token[at] = uint16_t(group * 64 + lane);
             s_slot[at] = slot[i];
             s_weight[at] = weight[i];
+            if (blockIdx.x == 0) to.list[int64_t(a) * ch.tokens + at] = make_int2(group * 64 + lane, slot[i]);
         }
     }
     for (int c = 0; c < kTokensMax / 64; ++c) mine += s_counts[c];
+    if (blockIdx.x == 0 && tid == 0) to.bounds[int64_t(a) * (kGroups + 1) + kGroups] = mine;
     __syncthreads();
 
     const int r = lane & 15, g = lane >> 4;
     const int f0 = int(blockIdx.x) * 16, f = min(f0 + r, hidden - 1);
     const Row<W> rows[2] = {gate.row(e, f), up.row(e, f)};
     const int chunks = (width + kChunkK - 1) / kChunkK;
-    for (int first = 0; first < mine; first += 16 * MT) {
-        Row<X> tokens[MT];
-        uint32_t tiles = 0;
+    const int c0 = chunks * wave / kUpWaves, c1 = chunks * (wave + 1) / kUpWaves;
+    const bool last = blockIdx.x == gridDim.x - 1;
+    // up to 16 MT tokens from `first` on
+    auto pass = [&](auto mt, auto in_flight, int first) {
+        constexpr int N = decltype(mt)::value;
+        Row<X> tokens[N];
+        const int tiles = min(N, (mine - first + 15) / 16);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int at = first + 16 * m;
-            if (at < mine) tiles |= 1u << m;
-            tokens[m] = {x + int64_t(s_token[min(at + r, mine - 1)]) * ld_x};
-        }
-        f32x4 acc[2][MT] = {};
-        accumulate<(MT == 1 ? 2 : 1)>(acc, rows, tokens, chunks * wave / kUpWaves, chunks * (wave + 1) / kUpWaves, width,
-                                      g, tiles);
+        for (int m = 0; m < N; ++m)
+            tokens[m] = {x + int64_t(s_token[min(first + 16 * m + r, mine - 1)]) * ld_x};
+        f32x4 acc[2][N] = {};
+        accumulate<decltype(in_flight)::value>(acc, rows, tokens, c0, c1, width, g, tiles);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (!(tiles >> m & 1)) continue;
+        for (int m = 0; m < N; ++m) {
+            if (m >= tiles) continue;
             parts[wave][0][lane] = acc[0][m];
             parts[wave][1][lane] = acc[1][m];
             __syncthreads();
@@ -178,76 +187,106 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
                 f32x4 sg = parts[0][0][lane], su = parts[0][1][lane];
 #pragma unroll
                 for (int v = 1; v < kUpWaves; ++v) sg += parts[v][0][lane], su += parts[v][1][lane];
-                const int64_t base = int64_t(s_slot[at]) * hidden;
+                const int64_t base = s_slot[at] * to.padded + f0 + 4 * g;
+                bf16x4 hi, lo;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int ff = f0 + 4 * g + i;
-                    if (ff >= hidden) break;
-                    const float h = s_weight[at] * (activate<GELU>(sg[i]) * su[i]);
-                    const bf16 top = bf16(h);
-                    to.hi[base + ff] = top;
+                    const float h = f0 + 4 * g + i < hidden ? s_weight[at] * (activate<GELU>(sg[i]) * su[i]) : 0.0f;
+                    hi[i] = bf16(h);
                     // an infinity has no second part
-                    to.lo[base + ff] = __builtin_isinf(float(top)) ? bf16(0.0f) : bf16(h - float(top));
+                    lo[i] = __builtin_isinf(float(hi[i])) ? bf16(0.0f) : bf16(h - float(hi[i]));
                 }
+                *reinterpret_cast<bf16x4 *>(to.hi + base) = hi;
+                *reinterpret_cast<bf16x4 *>(to.lo + base) = lo;
+                if (last)  // zeros to the end of the last chunk
+                    for (int64_t f = 16; f0 + f < to.padded; f += 16) {
+                        *reinterpret_cast<bf16x4 *>(to.hi + base + f) = bf16x4{};
+                        *reinterpret_cast<bf16x4 *>(to.lo + base + f) = bf16x4{};
+                    }
             }
             __syncthreads();
         }
+    };
+    using std::integral_constant;
+    for (int first = 0; first < mine; first += 16 * MT) {
+        if (MT > 1 && mine - first > 16) pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
+        else pass(integral_constant<int, 1>{}, integral_constant<int, (std::is_same_v<W, Mx4> ? 4 : 2)>{}, first);
     }
 }
 
+// A wave takes an equal run of the contraction over (expert in use, chunk of hidden units) for 16 columns, the tokens
+// of an expert 16 MT at a time, and adds each expert's results to its own sums of every token, in LDS.
 template <typename W, typename X, int MT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Between from, Matrix<W> down, int tokens, int hidden,
                                                                   int width, X *__restrict__ out, int64_t ld_out) {
-    __shared__ f32x4 parts[kDownWaves][64];
+    extern __shared__ __align__(16) char smem[];
+    f32x4 *sums = reinterpret_cast<f32x4 *>(smem);  // [wave][token][4 columns]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int n0 = int(blockIdx.x) * 16, t0 = int(blockIdx.y) * 16 * MT;
+    const int n0 = int(blockIdx.x) * 16, group = blockIdx.y, t0 = group * kGroup;
+    const int count = min(kGroup, tokens - t0);
     const int n = min(n0 + r, width - 1);
+    f32x4 *own = sums + wave * count * 4;
+    for (int i = lane; i < count * 4; i += 64) own[i] = f32x4{};
     const int chunks = (hidden + kChunkK - 1) / kChunkK;
-    // the contraction over (expert, hidden unit) in chunks, an equal run of them a wave
     const int64_t all = int64_t(*from.count) * chunks;
     int64_t u = all * wave / kDownWaves;
     const int64_t end = all * (wave + 1) / kDownWaves;
-    f32x4 acc[1][MT] = {};
-    while (u < end) {
-        const int a = int(u / chunks), c0 = int(u - int64_t(a) * chunks);
-        const int c1 = int(min(int64_t(chunks), c0 + (end - u)));
+    // an expert's number, list and first token of the list are loaded while the one before is multiplied
+    struct Next {
+        int expert, first, last;
+        int2 entry;
+    };
+    auto look = [&](int a) {
+        const int *b = from.bounds + int64_t(a) * (kGroups + 1) + group;
+        Next x{from.expert[a], b[0], b[1], make_int2(0, 0)};
+        x.entry = from.list[int64_t(a) * tokens + max(min(x.first + r, x.last - 1), 0)];
+        return x;
+    };
+    int a = int(u / chunks);
+    Next next{};
+    if (u < end) next = look(a);
+    for (; u < end; ++a) {
+        const Next now = next;
+        const int c0 = int(u - int64_t(a) * chunks), c1 = int(min(int64_t(chunks), c0 + (end - u)));
         u += c1 - c0;
-        Row<Planes> x[MT];
-        uint32_t tiles = 0;
+        if (u < end) next = look(a + 1);
+        const Row<W> rows[1] = {down.row(now.expert, n)};
+        auto pass = [&](auto mt, auto in_flight, int first) {
+            constexpr int N = decltype(mt)::value;
+            Row<Planes> x[N];
+            int2 entry[N];
+            const int tiles = min(N, (now.last - first + 15) / 16);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int t = t0 + 16 * m + r;
-            const int slot = t < tokens ? from.slot[int64_t(a) * tokens + t] : -1;
-            const int64_t base = int64_t(max(slot, 0)) * hidden;
-            x[m] = {from.hi + base, from.lo + base, slot >= 0};
-            if (__any(slot >= 0)) tiles |= 1u << m;
+            for (int m = 0; m < N; ++m) {
+                entry[m] = m == 0 && first == now.first
+                               ? now.entry
+                               : from.list[int64_t(a) * tokens + min(first + 16 * m + r, now.last - 1)];
+                const int64_t base = entry[m].y * from.padded;
+                x[m] = {from.hi + base, from.lo + base};
+            }
+            f32x4 part[1][N] = {};
+            accumulate<decltype(in_flight)::value>(part, rows, x, c0, c1, hidden, g, tiles);
+#pragma unroll
+            for (int m = 0; m < N; ++m)
+                if (first + 16 * m + r < now.last) own[(entry[m].x - t0) * 4 + g] += part[0][m];
+        };
+        using std::integral_constant;
+        for (int first = now.first; first < now.last; first += 16 * MT) {
+            if (MT > 1 && now.last - first > 16) pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
+            else pass(integral_constant<int, 1>{}, integral_constant<int, 2>{}, first);
         }
-        if (!tiles) continue;
-        const Row<W> rows[1] = {down.row(from.expert[a], n)};
-        f32x4 part[1][MT] = {};
-        accumulate<(MT == 1 ? 2 : 1)>(part, rows, x, c0, c1, hidden, g, tiles);
-        // a lane's results are its own token's: one not sent to this expert keeps its sum, whatever zeros times the
-        // expert's weights gave
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[0][m][i] = x[m].live ? acc[0][m][i] + part[0][m][i] : acc[0][m][i];
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < count * 4; i += 64 * kDownWaves) {
+        f32x4 sum = sums[i];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        if (m) __syncthreads();
-        parts[wave][lane] = acc[0][m];
-        __syncthreads();
-        const int t = t0 + 16 * m + r;
-        if (wave == 0 && t < tokens) {
-            f32x4 sum = parts[0][lane];
+        for (int v = 1; v < kDownWaves; ++v) sum += sums[v * count * 4 + i];
+        const int c = n0 + 4 * (i & 3);
+        X *o = out + int64_t(t0 + i / 4) * ld_out + c;
 #pragma unroll
-            for (int v = 1; v < kDownWaves; ++v) sum += parts[v][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n0 + 4 * g + i < width) out[t * ld_out + n0 + 4 * g + i] = rounded<X>(sum[i]);
-        }
+        for (int e = 0; e < 4; ++e)
+            if (c + e < width) o[e] = rounded<X>(sum[e]);
     }
 }
 
@@ -266,14 +305,18 @@ size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, voi
         at += up256(bytes);
         return p + a;
     };
-    char *count = take(4), *expert = take(size_t(most) * 4), *slot = take(size_t(most) * size_t(tokens) * 4);
-    char *hi = take(size_t(slots) * size_t(hidden) * 2), *lo = take(size_t(slots) * size_t(hidden) * 2);
+    const int64_t padded = (hidden + kChunkK - 1) / kChunkK * kChunkK;
+    char *count = take(4), *expert = take(size_t(most) * 4), *bounds = take(size_t(most) * (kGroups + 1) * 4);
+    char *list = take(size_t(most) * size_t(tokens) * 8);
+    char *hi = take(size_t(slots) * size_t(padded) * 2), *lo = take(size_t(slots) * size_t(padded) * 2);
     if (to) {
         to->count = reinterpret_cast<int *>(count);
         to->expert = reinterpret_cast<int *>(expert);
-        to->slot = reinterpret_cast<int *>(slot);
+        to->bounds = reinterpret_cast<int *>(bounds);
+        to->list = reinterpret_cast<int2 *>(list);
         to->hi = reinterpret_cast<bf16 *>(hi);
         to->lo = reinterpret_cast<bf16 *>(lo);
+        to->padded = padded;
     }
     return at;
 }
@@ -305,8 +348,10 @@ void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matr
                            matrix<W>(up), width, hidden, b);
     auto go = [&](auto mt) {
         constexpr int MT = decltype(mt)::value;
-        hipLaunchKernelGGL((k_experts_down<W, X, MT>), dim3((width + 15) / 16, (ch.tokens + 16 * MT - 1) / (16 * MT)),
-                           dim3(64 * kDownWaves), 0, s, b, matrix<W>(down), ch.tokens, hidden, width, out, ld_out);
+        const size_t lds = size_t(kDownWaves) * std::min(ch.tokens, kGroup) * 64;
+        allow_lds(reinterpret_cast<const void *>(&k_experts_down<W, X, MT>), lds);
+        hipLaunchKernelGGL((k_experts_down<W, X, MT>), dim3((width + 15) / 16, (ch.tokens + kGroup - 1) / kGroup),
+                           dim3(64 * kDownWaves), lds, s, b, matrix<W>(down), ch.tokens, hidden, width, out, ld_out);
     };
     if (ch.tokens <= 16) go(std::integral_constant<int, 1>{});
     else go(std::integral_constant<int, 4>{});

@@ -1,11 +1,13 @@
 // Products with few tokens: one wave takes 16 rows of each of R matrices and 16 MT tokens over a range of the
-// contraction, the rows as the first operand of the 16 x 16 matrix instructions and the tokens as the second, so that
-// weights go from memory to registers once and are bound by memory, whatever the number of tokens.
+// contraction, the rows as the first operand of the 16 x 16 matrix instructions and the tokens as the second. Weights
+// go from memory to registers once; what bounds such a product is their bytes, whatever the number of tokens.
 //
 // A chunk is 128 values of the contraction, four instructions. Lane (r, g) = (lane % 16, lane / 16) holds row r (token
-// r) at 32 values of the chunk. Which ones is free as long as both operands agree: for 4-bit rows it is block g, 16
-// bytes under one scale; for 16-bit rows instruction j takes 8 values at 32 j + 8 g, so that the four lanes of a row
-// read 64 bytes in a row. A result's lane (t, q) holds rows 4 q .. 4 q + 3 for token t.
+// r); instruction j takes its 8 values at 32 j + 8 g, so that the four lanes of a row read 64 bytes in a row. 4-bit
+// rows are read as one block a lane, 16 bytes, and four exchanges between lanes turn block g into a part of every
+// block: with a block a lane instead, the tokens would come in pieces of 16 bytes 64 apart, twice as many cache lines
+// an instruction (37 tokens through 5,003 x 4,001: 30 us for 17). A result's lane (t, q) holds rows 4 q .. 4 q + 3 for
+// token t.
 #pragma once
 
 #include "mx4.hpp"
@@ -23,9 +25,8 @@ struct Row<Mx4> {
     const uint8_t *codes, *scales;
 };
 template <>
-struct Row<Planes> {
+struct Row<Planes> {  // whole chunks: zeros past the width
     const bf16 *hi, *lo;
-    bool live;  // a row that is not counts as zeros and is not read
 };
 
 template <typename T>
@@ -35,161 +36,258 @@ struct Piece {  // a lane's part of a chunk
 template <>
 struct Piece<Mx4> {
     i32x4 codes;
-    uint32_t scale;
+    uint32_t scale;  // of block g; as a matrix of 16-bit tokens, of the four blocks
 };
 template <>
 struct Piece<Planes> {
     i32x4 hi[4], lo[4];
 };
 
-// A lane's 8 values of 16 bits at p, those from the width on as zeros.
-template <typename T>
-__device__ __forceinline__ i32x4 load_half(const T *p, int k, int width) {
-    if (k + 8 <= width) return *reinterpret_cast<const Half16 *>(p + k);
-    i32x4 v{};
-    if (k >= width) return v;
-    const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+// Eight 16-bit values at k of a row, those from the width on as zeros: loaded where the row still has eight and moved.
+__device__ __forceinline__ i32x4 load_half(const uint16_t *p, int k, int width) {
+    using Wide = unsigned __int128;
+    if (width < 8) {
+        i32x4 v{};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t e = k + i < width ? h[k + i] : 0;
-        v[i / 2] |= int32_t(e << (16 * (i & 1)));
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t e = p[min(i, width - 1)];
+            v[i / 2] |= int32_t((k + i < width ? e : 0) << (16 * (i & 1)));
+        }
+        return v;
     }
-    return v;
+    const int at = min(k, width - 8);
+    const Wide v = bits_as<Wide>(i32x4(*reinterpret_cast<const Half16 *>(p + at)));
+    return bits_as<i32x4>(k - at < 8 ? v >> (16 * (k - at)) : Wide(0));
 }
 
-// WHOLE: the chunk at k lies within the width. BY_BLOCKS: the lanes' values go by blocks of 32.
-template <bool WHOLE, bool BY_BLOCKS, typename T>
-__device__ __forceinline__ void load_piece(Piece<T> &out, const Row<T> &row, int k, int width, int g) {
+// A whole chunk of a row or token. BOTH: both sides are of 4 bits.
+template <bool BOTH, typename T>
+__device__ __forceinline__ void load_piece(Piece<T> &out, const Row<T> &row, int k, int g) {
     if constexpr (std::is_same_v<T, Mx4>) {
-        const int b = k / kBlock + g;
-        if (WHOLE || b * kBlock < width) {
-            out.codes = *reinterpret_cast<const Byte16 *>(row.codes + int64_t(b) * kBlockBytes);
-            out.scale = row.scales[b];
-        } else {
-            out.codes = i32x4{};
-            out.scale = 127;
-        }
+        const int b = k / kBlock;
+        out.codes = *reinterpret_cast<const Byte16 *>(row.codes + int64_t(b + g) * kBlockBytes);
+        if constexpr (BOTH) out.scale = row.scales[b + g];
+        else out.scale = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(row.scales + b);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int at = k + (BY_BLOCKS ? 32 * g + 8 * j : 32 * j + 8 * g);
+            const int at = k + 32 * j + 8 * g;
             if constexpr (std::is_same_v<T, Planes>) {
-                if (!row.live) {
-                    out.hi[j] = out.lo[j] = i32x4{};
-                } else if (WHOLE) {
-                    out.hi[j] = *reinterpret_cast<const Half16 *>(row.hi + at);
-                    out.lo[j] = *reinterpret_cast<const Half16 *>(row.lo + at);
-                } else {
-                    out.hi[j] = load_half(row.hi, at, width);
-                    out.lo[j] = load_half(row.lo, at, width);
-                }
+                out.hi[j] = *reinterpret_cast<const i32x4 *>(row.hi + at);
+                out.lo[j] = *reinterpret_cast<const i32x4 *>(row.lo + at);
             } else {
-                if (WHOLE) out.v[j] = *reinterpret_cast<const Half16 *>(row.p + at);
-                else out.v[j] = load_half(row.p, at, width);
+                out.v[j] = *reinterpret_cast<const Half16 *>(row.p + at);
             }
         }
     }
 }
 
-// One tile of 16 tokens, number m of the sums. Conversions of the weights that another tile repeats are the same
-// expressions, made once.
-template <typename W, typename X, int R, int MT>
-__device__ __forceinline__ void multiply(f32x4 (&acc)[R][MT], int m, const Piece<W> (&w)[R], const Piece<X> &x) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        f32x4 &a = acc[i][m];
-        if constexpr (std::is_same_v<X, Mx4>) {
-            a = mma16_mx4<0>(w[i].codes, w[i].scale, x.codes, x.scale, a);
-        } else if constexpr (std::is_same_v<W, Mx4>) {
-            const float s = scale_operand(w[i].scale);
-            if constexpr (std::is_same_v<X, f16>) {
-                // float16 tokens meet the weights in float16 where it holds them exactly, which it does for all but
-                // far scales; else in two bfloat16 parts
-                const i32x4 c = w[i].codes;
-                const bool none = (c[0] | c[1] | c[2] | c[3]) == 0 && w[i].scale != 255;
-                if (__all(f16_scale(w[i].scale) || none)) {
-                    const float s16 = none ? 1.0f : s;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) a = mma16<f16>(widen<f16>(uint32_t(c[j]), s16), x.v[j], a);
-                    continue;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const i32x4 v = widen<bf16>(uint32_t(w[i].codes[j]), s);
-                if constexpr (std::is_same_v<X, bf16>) {
-                    a = mma16<bf16>(v, x.v[j], a);
-                } else {
-                    i32x4 hi, lo;
-                    if constexpr (std::is_same_v<X, Planes>) hi = x.hi[j], lo = x.lo[j];
-                    else split(x.v[j], hi, lo);
-                    a = mma16<bf16>(v, hi, a);
-                    a = mma16<bf16>(v, lo, a);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (!std::is_same_v<X, Planes>) {
-                    a = mma16<W>(w[i].v[j], x.v[j], a);
-                } else if constexpr (std::is_same_v<W, bf16>) {
-                    a = mma16<bf16>(w[i].v[j], x.hi[j], a);
-                    a = mma16<bf16>(w[i].v[j], x.lo[j], a);
-                } else {
-                    i32x4 hi, lo;
-                    split(w[i].v[j], hi, lo);
-                    a = mma16<bf16>(hi, x.hi[j], a);
-                    a = mma16<bf16>(hi, x.lo[j], a);
-                    // the product of both second parts lies 2^-16 and less under that of the first
-                    a = mma16<bf16>(lo, x.hi[j], a);
-                }
-            }
-        }
+// A lane's 8 values of a token for one instruction.
+template <typename T>
+struct Step {
+    i32x4 hi, lo;  // 16-bit tokens: hi alone
+};
+
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Step<T> load_step(const Row<T> &row, int k, int width) {
+    Step<T> s;
+    if constexpr (std::is_same_v<T, Planes>) {
+        s.hi = *reinterpret_cast<const i32x4 *>(row.hi + k);
+        s.lo = *reinterpret_cast<const i32x4 *>(row.lo + k);
+    } else if (WHOLE) {
+        s.hi = *reinterpret_cast<const Half16 *>(row.p + k);
+    } else {
+        s.hi = load_half(reinterpret_cast<const uint16_t *>(row.p), k, width);
+    }
+    return s;
+}
+
+// Word w of lane g becomes word g of lane w.
+__device__ __forceinline__ i32x4 exchange(i32x4 v) {
+    using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+    const u32x2 a = __builtin_amdgcn_permlane32_swap(uint32_t(v[0]), uint32_t(v[2]), false, false);
+    const u32x2 b = __builtin_amdgcn_permlane32_swap(uint32_t(v[1]), uint32_t(v[3]), false, false);
+    const u32x2 c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const u32x2 d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return i32x4{int32_t(c[0]), int32_t(c[1]), int32_t(d[0]), int32_t(d[1])};
+}
+
+__device__ __forceinline__ float scale_operand_of(uint32_t scales, int j) {
+    return scale_operand(scales >> (8 * j) & 255);
+}
+
+// One instruction's worth of a matrix's rows, a (of type T: its own, or what its codes were widened to), and a token
+// tile: as many instructions as the two have parts.
+template <typename T, typename X>
+__device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 c) {
+    if constexpr (std::is_same_v<X, T>) {
+        return mma16<T>(a, x.hi, c);
+    } else if constexpr (std::is_same_v<X, Planes>) {
+        i32x4 hi = a, lo;
+        if constexpr (std::is_same_v<T, f16>) split(a, hi, lo);
+        c = mma16<bf16>(hi, x.hi, c);
+        c = mma16<bf16>(hi, x.lo, c);
+        // the product of both second parts lies 2^-16 and less under that of the first
+        if constexpr (std::is_same_v<T, f16>) c = mma16<bf16>(lo, x.hi, c);
+        return c;
+    } else {  // float16 tokens, bfloat16 rows
+        i32x4 hi, lo;
+        split(x.hi, hi, lo);
+        c = mma16<bf16>(a, hi, c);
+        return mma16<bf16>(a, lo, c);
     }
 }
 
-// acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values. tiles: a bit for each tile of
-// 16 tokens that counts; the others are neither read nor multiplied.
+// Whether float16 holds every value of a wave's chunk of a matrix: blocks of zeros do not count.
+__device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) {
+    const uint32_t b = w.scale >> (8 * g) & 255;
+    return __all(f16_scale(b) || ((w.codes[0] | w.codes[1] | w.codes[2] | w.codes[3]) == 0 && b != 255));
+}
+
+// acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values, U chunks of rows in flight.
+// Tiles of tokens from `tiles` on are neither read nor multiplied. One tile's tokens are loaded with the rows, those of
+// several beside the products, which would need more registers than there are otherwise.
 template <int U, typename W, typename X, int R, int MT>
 __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&rows)[R], const Row<X> (&x)[MT], int c0,
-                                           int c1, int width, int g, uint32_t tiles) {
-    constexpr bool BY_BLOCKS = std::is_same_v<W, Mx4>;
-    const int whole = width / kChunkK < c1 ? width / kChunkK : c1;
-    // tokens that fill more registers than this are loaded tile by tile beside the products
-    constexpr bool AT_ONCE = U * MT * sizeof(Piece<X>) <= 64 * 4;
+                                           int c1, int width, int g, int tiles = MT) {
+    constexpr bool BOTH = std::is_same_v<X, Mx4>, CODES = std::is_same_v<W, Mx4>;
+    const int whole = min(width / kChunkK, c1);
     int c = c0;
-    for (; c + U <= whole; c += U) {
-        Piece<W> w[U][R];
-        Piece<X> t[U][MT];
+    auto some = [&](auto count) {
+        constexpr int N = decltype(count)::value;
+        Piece<W> w[N][R];
+        Piece<X> t[N][MT];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < N; ++u) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) load_piece<true, BY_BLOCKS>(w[u][i], rows[i], (c + u) * kChunkK, width, g);
-            if constexpr (AT_ONCE) {
+            for (int i = 0; i < R; ++i) load_piece<BOTH>(w[u][i], rows[i], (c + u) * kChunkK, g);
+            if constexpr (BOTH || MT == 1) {
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
-                    if (tiles >> m & 1) load_piece<true, BY_BLOCKS>(t[u][m], x[m], (c + u) * kChunkK, width, g);
+                    if (m < tiles) load_piece<BOTH>(t[u][m], x[m], (c + u) * kChunkK, g);
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < N; ++u) {
+            if constexpr (BOTH) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (!(tiles >> m & 1)) continue;
-                if constexpr (!AT_ONCE) load_piece<true, BY_BLOCKS>(t[u][m], x[m], (c + u) * kChunkK, width, g);
-                multiply<W, X>(acc, m, w[u], t[u][m]);
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+                        if (m < tiles)
+                            acc[i][m] = mma16_mx4<0>(w[u][i].codes, w[u][i].scale, t[u][m].codes, t[u][m].scale,
+                                                     acc[i][m]);
+            } else {
+                i32x4 codes[R];
+                if constexpr (CODES) {
+#pragma unroll
+                    for (int i = 0; i < R; ++i) codes[i] = exchange(w[u][i].codes);
+                }
+                auto chunk = [&](auto type) {
+                    using T = decltype(type);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        i32x4 a[R];
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            if constexpr (CODES)
+                                a[i] = widen<T>(uint32_t(codes[i][j]), scale_operand_of(w[u][i].scale, j));
+                            else a[i] = w[u][i].v[j];
+                        }
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            if (m >= tiles) continue;
+                            Step<X> s;
+                            if constexpr (MT > 1)
+                                s = load_step<true>(x[m], (c + u) * kChunkK + 32 * j + 8 * g, width);
+                            else if constexpr (std::is_same_v<X, Planes>) s.hi = t[u][m].hi[j], s.lo = t[u][m].lo[j];
+                            else s.hi = t[u][m].v[j];
+#pragma unroll
+                            for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[i], s, acc[i][m]);
+                        }
+                    }
+                };
+                if constexpr (!CODES) {
+                    chunk(W{});
+                } else if constexpr (std::is_same_v<X, f16>) {
+                    // float16 tokens meet the weights in float16 where it holds them exactly, which it does for all
+                    // but far scales; else in two bfloat16 parts
+                    bool exact = true;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) exact = exact && f16_holds(w[u][i], g);
+                    if (exact) chunk(f16{});
+                    else chunk(bf16{});
+                } else {
+                    chunk(bf16{});
+                }
             }
-    }
-    for (; c < c1; ++c) {
-        Piece<W> w[R];
+        }
+        c += N;
+    };
+    while (c + U <= whole) some(std::integral_constant<int, U>{});
+    if constexpr (U > 1)
+        while (c < whole) some(std::integral_constant<int, 1>{});
+    if (c >= c1) return;
+    // the last chunk, in parts: what lies past the width is zeros on both sides
+    if constexpr (BOTH) {
+        const int b = c * (kChunkK / kBlock) + g;
+        const bool here = b * kBlock < width;
+        auto part = [&](const Row<Mx4> &row) {
+            Piece<Mx4> p{i32x4{}, 127};
+            if (here) {
+                p.codes = *reinterpret_cast<const Byte16 *>(row.codes + int64_t(b) * kBlockBytes);
+                p.scale = row.scales[b];
+            }
+            return p;
+        };
+        Piece<Mx4> w[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) load_piece<false, BY_BLOCKS>(w[i], rows[i], c * kChunkK, width, g);
+        for (int i = 0; i < R; ++i) w[i] = part(rows[i]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            if (!(tiles >> m & 1)) continue;
-            Piece<X> t;
-            load_piece<false, BY_BLOCKS>(t, x[m], c * kChunkK, width, g);
-            multiply<W, X>(acc, m, w, t);
+            if (m >= tiles) continue;
+            const Piece<Mx4> t = part(x[m]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) acc[i][m] = mma16_mx4<0>(w[i].codes, w[i].scale, t.codes, t.scale, acc[i][m]);
+        }
+    } else {
+#pragma unroll 1
+        for (int k = c * kChunkK; k < width; k += kBlock) {
+            i32x4 a[R];
+            uint32_t word[R], top[R];
+            bool exact = true;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                if constexpr (CODES) {
+                    const uint8_t *p = rows[i].codes + int64_t(k / kBlock) * kBlockBytes + 4 * g;
+                    word[i] = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(p);
+                    top[i] = rows[i].scales[k / kBlock];
+                    exact = exact && f16_scale(top[i]);
+                } else {
+                    a[i] = load_half(reinterpret_cast<const uint16_t *>(rows[i].p), k + 8 * g, width);
+                }
+            }
+            auto part = [&](auto type) {
+                using T = decltype(type);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if constexpr (CODES) a[i] = widen<T>(word[i], scale_operand(top[i]));
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (m >= tiles) continue;
+                    const Step<X> s = load_step<false>(x[m], k + 8 * g, width);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[i], s, acc[i][m]);
+                }
+            };
+            if constexpr (!CODES) {
+                part(W{});
+            } else if constexpr (std::is_same_v<X, f16>) {
+                if (__all(exact)) part(f16{});
+                else part(bf16{});
+            } else {
+                part(bf16{});
+            }
         }
     }
 }

@@ -24,6 +24,7 @@ using f32x2 = float __attribute__((ext_vector_type(2)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using bf16x4 = __bf16 __attribute__((ext_vector_type(4)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));

@@ -12,7 +12,7 @@
 // codes under one scale.
 #pragma once
 
-#include "mx4.hpp"
+#include "few.hpp"
 
 namespace vspmm {
 
@@ -25,16 +25,8 @@ __device__ __forceinline__ int place(int row, int chunk) { return row * 8 + (chu
 
 // Eight 16-bit values at k of a row, those from the width on as zeros. `whole`: none are.
 __device__ __forceinline__ i32x4 load_chunk(const uint16_t *row, int k, int width, bool whole) {
-    if (whole || k + 8 <= width) return *reinterpret_cast<const Half16 *>(row + k);
-    i32x4 v{};
-    if (k < width) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t e = k + i < width ? row[k + i] : 0;
-            v[i / 2] |= int32_t(e << (16 * (i & 1)));
-        }
-    }
-    return v;
+    if (whole) return *reinterpret_cast<const Half16 *>(row + k);
+    return load_half(row, k, width);
 }
 
 struct TileShape {
