@@ -138,11 +138,8 @@ __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 
     }
 }
 
-// Whether float16 holds every value of a wave's chunk of a matrix: blocks of zeros do not count.
-__device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) {
-    const uint32_t b = w.scale >> (8 * g) & 255;
-    return __all(f16_scale(b) || ((w.codes[0] | w.codes[1] | w.codes[2] | w.codes[3]) == 0 && b != 255));
-}
+// Whether a wave's chunk of a matrix may meet its tokens in float16: each lane answers for the block it loaded.
+__device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) { return __all(f16_scale(w.scale >> (8 * g) & 255)); }
 
 // acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values, U chunks of rows in flight.
 // Tiles of tokens from `tiles` on are neither read nor multiplied. One tile's tokens are loaded with the rows, those of

@@ -63,9 +63,10 @@ __device__ __forceinline__ i32x4 widen(uint32_t codes, float scale) {
     return r;
 }
 
-// Whether float16 holds every value of a block of this scale exactly: 0.5 * 2^-23 is its least subnormal and
-// 6 * 2^13 lies below its largest number.
-__device__ __forceinline__ bool f16_scale(uint32_t b) { return b - 104u <= 36u; }
+// Whether a product with float16 tokens may take a block of this scale in float16: it holds all of the block's values
+// (0.5 * 2^-23 is its least subnormal, 6 * 2^13 lies below its largest number), or they are so small, as in a block of
+// zeros, that 2^24 of them times the largest token stay 2^14 times under half of the result's least subnormal.
+__device__ __forceinline__ bool f16_scale(uint32_t b) { return b - 104u <= 36u || b <= 40u; }
 
 // Eight float16 values as the sum of two bfloat16 each: the upper eight bits of the significand, and the rest, which
 // has at most three. Exact: float16's least subnormal is a normal bfloat16. An infinity or NaN goes into the first.

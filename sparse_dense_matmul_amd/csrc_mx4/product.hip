@@ -9,6 +9,7 @@
 #include "few.hpp"
 #include "host.hpp"
 #include "quantize.hpp"
+#include "stream.hpp"
 #include "tile.hpp"
 
 using namespace vspmm;
@@ -121,6 +122,16 @@ void with_tile(int64_t m, int64_t n, F &&f) {
     }
 }
 
+bool streams(const vspmm_mx4 &a) {
+    const auto bits = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
+    return ((bits(a.codes) | a.ld_codes) & 15) == 0 && ((bits(a.scales) | a.ld_scales) & 15) == 0 &&
+           a.ld_codes < (1 << 24) && a.ld_scales < (1 << 24);
+}
+
+bool streams(const void *x, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (ld & 7) == 0 && ld < (1 << 22);
+}
+
 TileShape tile_shape(int64_t m, int64_t n, int64_t k, int edge, unsigned &tiles) {
     const int64_t tn = (n + edge - 1) / edge;
     tiles = unsigned(((m + edge - 1) / edge) * tn);
@@ -200,6 +211,14 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
             launch_few(Row<T>{static_cast<const T *>(x)}, ld_x, 0, *w, o, ld_out, int(m), int(n), int(width), stream);
             return launched();
         }
+        if (m >= 256 && n >= 256 && width % 512 == 0 && tile_width(m, n) == 4 && streams(x, ld_x) && streams(*w)) {
+            unsigned tiles;
+            const TileShape s = tile_shape(m, n, width, 256, tiles);
+            allow_lds(reinterpret_cast<const void *>(&k_stream<T>), kStreamLds);
+            hipLaunchKernelGGL((k_stream<T>), dim3(tiles), dim3(256), kStreamLds, stream, static_cast<const T *>(x), ld_x,
+                               w->codes, w->ld_codes, w->scales, w->ld_scales, o, ld_out, s);
+            return launched();
+        }
         with_tile(m, n, [&](auto tw) {
             constexpr int TW = decltype(tw)::value;
             unsigned tiles;
@@ -253,6 +272,15 @@ vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t w
         if (m <= kFewTokens) {
             launch_few(Row<Mx4>{x->codes, x->scales}, x->ld_codes, x->ld_scales, *w, o, ld_out, int(m), int(n),
                        int(width), stream);
+            return launched();
+        }
+        if (m >= 256 && n >= 256 && width % (2 * kStepCodes) == 0 && tile_width(m, n) == 4 && streams(*x) && streams(*w)) {
+            unsigned tiles;
+            const TileShape s = tile_shape(m, n, width, 256, tiles);
+            allow_lds(reinterpret_cast<const void *>(&k_stream_both<T>), kStreamBothLds);
+            hipLaunchKernelGGL((k_stream_both<T>), dim3(tiles), dim3(256), kStreamBothLds, stream, x->codes,
+                               x->ld_codes, x->scales, x->ld_scales, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
+                               ld_out, s);
             return launched();
         }
         with_tile(m, n, [&](auto tw) {

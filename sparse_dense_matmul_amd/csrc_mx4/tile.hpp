@@ -245,9 +245,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(const X *__restrict__ x, 
             const uint32_t b = reinterpret_cast<const uint8_t *>(lds_s + buf * EDGE + wn + 32 * i + r)[g];
             sc[i] = scale_operand(b);
             if constexpr (std::is_same_v<X, f16>) {
-                const bool none = (c[i][0] | c[i][1] | c[i][2] | c[i][3]) == 0 && b != 255;
-                exact16 = exact16 && (none || f16_scale(b));
-                if (none) sc[i] = 1.0f;
+                exact16 = exact16 && f16_scale(b);
             }
         }
         auto step = [&](auto type, auto halves) {
