@@ -124,7 +124,7 @@ void with_tile(int64_t m, int64_t n, F &&f) {
 
 bool streams(const vspmm_mx4 &a) {
     const auto bits = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
-    return ((bits(a.codes) | a.ld_codes) & 15) == 0 && ((bits(a.scales) | a.ld_scales) & 15) == 0 &&
+    return ((bits(a.codes) | a.ld_codes) & 15) == 0 && ((bits(a.scales) | a.ld_scales) & 3) == 0 &&
            a.ld_codes < (1 << 24) && a.ld_scales < (1 << 24);
 }
 
@@ -211,7 +211,7 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
             launch_few(Row<T>{static_cast<const T *>(x)}, ld_x, 0, *w, o, ld_out, int(m), int(n), int(width), stream);
             return launched();
         }
-        if (m >= 256 && n >= 256 && width % 512 == 0 && tile_width(m, n) == 4 && streams(x, ld_x) && streams(*w)) {
+        if (m >= 256 && n >= 256 && width % kStepCodes == 0 && tile_width(m, n) == 4 && streams(x, ld_x) && streams(*w)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 256, tiles);
             allow_lds(reinterpret_cast<const void *>(&k_stream<T>), kStreamLds);
@@ -274,7 +274,7 @@ vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t w
                        int(width), stream);
             return launched();
         }
-        if (m >= 256 && n >= 256 && width % (2 * kStepCodes) == 0 && tile_width(m, n) == 4 && streams(*x) && streams(*w)) {
+        if (m >= 256 && n >= 256 && width % kStepCodes == 0 && tile_width(m, n) == 4 && streams(*x) && streams(*w)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 256, tiles);
             allow_lds(reinterpret_cast<const void *>(&k_stream_both<T>), kStreamBothLds);

@@ -10,8 +10,13 @@ using Lds = __attribute__((address_space(3))) char;
 // A wave's 64 pieces of BYTES bytes, each lane's at its own offset from a base and `more` beyond it, to consecutive
 // ones in LDS. The address's common part stays in scalar registers.
 using Buffer = __amdgpu_buffer_rsrc_t;
-__device__ __forceinline__ Buffer buffer_of(const uint8_t *p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, int(0x80000000u), 0x00020000);
+__device__ __forceinline__ Buffer buffer_of(const uint8_t *p, uint32_t bytes = 0x80000000u) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, int(bytes), 0x00020000);
+}
+// Rows of scales from row0 on: 16 bytes are copied where a row's last 8 are left, and past the last row are zeros.
+__device__ __forceinline__ Buffer scales_of(const uint8_t *p, int64_t ld, int row0, int rows, int blocks) {
+    const int64_t bytes = int64_t(rows - 1 - row0) * ld + blocks;
+    return buffer_of(p + row0 * ld, bytes < 0x80000000ll ? uint32_t(bytes) : 0x80000000u);
 }
 __device__ __forceinline__ void copy16(Buffer from, uint32_t offset, uint32_t more, Lds *to) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, int(offset),
@@ -47,6 +52,19 @@ __device__ __forceinline__ void mix() {
     }
 }
 
+// The same where an instruction's rows are widened beside the products, by VALU operations behind each from the
+// FIRST on.
+template <int READS, int COPIES, int FIRST, int VALU>
+__device__ __forceinline__ void mix_widening() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i < READS) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (i % 3 == 2 && i / 3 < COPIES) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        if (i >= FIRST) __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    }
+}
+
 constexpr int kStreamEdge = 256;
 constexpr size_t kStreamBothLds = 2 * 512 * (128 + 16);
 
@@ -79,7 +97,7 @@ __global__ __launch_bounds__(256, 1) void k_stream_both(const uint8_t *__restric
     };
     // scales go by two steps, 16 bytes a row: in each of the two a wave copies those of 64 of its 128 rows
     const int64_t lds_ = mine ? ld_xs : ld_scales;
-    const Buffer src_s = buffer_of((mine ? x_scales : scales) + row0 * lds_);
+    const Buffer src_s = scales_of(mine ? x_scales : scales, lds_, row0, mine ? s.m : s.n, s.k / kBlock);
     const uint32_t off_s = uint32_t(lane) * uint32_t(lds_), rows64 = 64 * uint32_t(lds_);
     const char *tops = smem + 2 * 512 * 128;
     Lds *to_s = (Lds *)tops + wave * 128 * 16;
@@ -197,7 +215,7 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
     const int64_t ld_xb = ld_x * 2;
     const Buffer src_x = buffer_of(reinterpret_cast<const uint8_t *>(x) + (m0 + 64 * wave) * ld_xb);
     const Buffer src_w = buffer_of(codes + (n0 + 64 * wave) * ld_codes);
-    const Buffer src_s = buffer_of(scales + (n0 + 64 * wave) * ld_scales);
+    const Buffer src_s = scales_of(scales, ld_scales, n0 + 64 * wave, s.n, s.k / kBlock);
     const uint32_t piece = 16 * ((lane & 7) ^ (lane >> 3));
     const uint32_t off_x = uint32_t(lane >> 3) * uint32_t(ld_xb), off_w = uint32_t(lane >> 3) * uint32_t(ld_codes);
     const uint32_t offs_x[2] = {off_x + piece, off_x + (piece ^ 16)}, offs_w[2] = {off_w + piece, off_w + (piece ^ 16)};
@@ -271,6 +289,7 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
 #pragma unroll
             for (int i = 3; i < 6; ++i) copy_x(next, 1 - P, i);
             multiply(0);
+            mix_widening<4, 3, 0, 1>();
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
             read(P, 0, 2);
@@ -278,12 +297,14 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
 #pragma unroll
             for (int i = 6; i < 8; ++i) copy_x(next, 1 - P, i);
             multiply(1);
+            mix_widening<4, 2, 0, 1>();
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
             read(P, 1, 3);
             widen_rows(1, 0, 3);
             copy_w(four, ~(it >> 2) & 1, 2 * (it & 3));
             multiply(0);
+            mix_widening<4, 2, 0, 1>();
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
             __syncthreads();
@@ -293,6 +314,7 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
 #pragma unroll
             for (int i = 0; i < 3; ++i) copy_x(second, P, i);
             multiply(1);
+            mix_widening<12, 3, 12, 5>();
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -306,10 +328,11 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
         // whether float16 holds the tile's rows: a thread looks at one row's scales
         const uint8_t *row = scales + int64_t(n0 + int(threadIdx.x)) * ld_scales;
         bool fine = true;
-        for (int i = 0; i < s.k / kBlock; i += 16) {
-            const i32x4 v = *reinterpret_cast<const i32x4 *>(row + i);
+        for (int i = 0; i < s.k / kBlock; i += 8) {
+            using Byte8 = int32_t __attribute__((ext_vector_type(2), aligned(1)));
+            const Byte8 v = *reinterpret_cast<const Byte8 *>(row + i);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) fine = fine && f16_scale(uint32_t(v[e / 4]) >> (8 * (e & 3)) & 255);
+            for (int e = 0; e < 8; ++e) fine = fine && f16_scale(uint32_t(v[e / 4]) >> (8 * (e & 3)) & 255);
         }
         if (__syncthreads_and(fine)) run(f16{});
         else run(bf16{});

@@ -12,7 +12,8 @@ from test_gpu_mx4 import TYPES, packed, small_matrix
 pytestmark = pytest.mark.gpu
 
 # rows and columns that tiles of 256 do not divide, widths of one to five copies of scales
-SHAPES = [(4096, 4096, 512), (3700, 3900, 1024), (257, 60000, 512), (50001, 300, 1536), (4000, 3841, 2560)]
+SHAPES = [(4096, 4096, 512), (3700, 3900, 1024), (257, 60000, 512), (50001, 300, 1536), (4000, 3841, 2560), (3601, 4100, 256), (4096, 4096, 768),
+          (8192, 2048, 1280)]
 
 
 def values(codes, scales, width, dev):
