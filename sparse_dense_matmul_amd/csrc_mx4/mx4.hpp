@@ -45,22 +45,26 @@ __device__ __forceinline__ T bits_as(F x) {
 // The scale operand of the conversions.
 __device__ __forceinline__ float scale_operand(uint32_t b) { return __uint_as_float(b << 23); }
 
+// Codes 2 H and 2 H + 1 of a word of eight as two values of 16 bits.
+template <typename T, int H>
+__device__ __forceinline__ int32_t widen_two(uint32_t codes, float scale) {
+    if constexpr (std::is_same_v<T, bf16>)
+        return bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, H));
+    else return bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, H));
+}
+template <typename T>
+__device__ __forceinline__ int32_t widen_pair(uint32_t codes, float scale, int h) {  // h: known when compiled
+    return h == 0   ? widen_two<T, 0>(codes, scale)
+           : h == 1 ? widen_two<T, 1>(codes, scale)
+           : h == 2 ? widen_two<T, 2>(codes, scale)
+                    : widen_two<T, 3>(codes, scale);
+}
+
 // Eight codes (a word) as eight values of 16 bits.
 template <typename T>
 __device__ __forceinline__ i32x4 widen(uint32_t codes, float scale) {
-    i32x4 r;
-    if constexpr (std::is_same_v<T, bf16>) {
-        r[0] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
-        r[1] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1));
-        r[2] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
-        r[3] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
-    } else {
-        r[0] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 0));
-        r[1] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 1));
-        r[2] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 2));
-        r[3] = bits_as<int32_t>(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, 3));
-    }
-    return r;
+    return i32x4{widen_two<T, 0>(codes, scale), widen_two<T, 1>(codes, scale), widen_two<T, 2>(codes, scale),
+                 widen_two<T, 3>(codes, scale)};
 }
 
 // Whether a product with float16 tokens may take a block of this scale in float16: it holds all of the block's values

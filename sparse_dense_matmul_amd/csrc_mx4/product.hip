@@ -244,6 +244,15 @@ vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t 
         using T = decltype(e);
         T *o = static_cast<T *>(grad);
         if (n == 0) return zero_rows(o, ld_grad, m, width, stream);
+        if (m >= 256 && n % kStepHalf == 0 && tile_width(m, width) == 4 && streams(dout, ld_dout)) {
+            unsigned tiles;
+            const TileShape s = tile_shape(m, width, n, 256, tiles);
+            allow_lds(reinterpret_cast<const void *>(&k_stream_grad<T>), kStreamGradLds);
+            hipLaunchKernelGGL((k_stream_grad<T>), dim3(tiles), dim3(256), kStreamGradLds, stream,
+                               static_cast<const T *>(dout), ld_dout, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
+                               ld_grad, s);
+            return launched();
+        }
         with_tile(m, width, [&](auto tw) {
             constexpr int TW = decltype(tw)::value;
             unsigned tiles;

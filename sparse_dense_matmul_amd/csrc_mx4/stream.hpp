@@ -344,4 +344,148 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
 }
 
+// The gradient: dx[m][c] = sum over n of dy[m][n] w[n][c], 256 tokens by 256 columns, 64 rows n a step. The tokens'
+// rows are copied as above. The matrix's codes go through registers: a thread takes eight columns of eight rows, a word
+// from each, widens them, joins pairs of rows and writes each column's eight values to its row in LDS. A step's words
+// are loaded a step ahead of that.
+constexpr size_t kStreamGradLds = 2 * 256 * (128 + 128);
+
+template <typename X>
+__global__ __launch_bounds__(256, 1) void k_stream_grad(const X *__restrict__ dy, int64_t ld_dy,
+                                                        const uint8_t *__restrict__ codes, int64_t ld_codes,
+                                                        const uint8_t *__restrict__ scales, int64_t ld_scales,
+                                                        X *__restrict__ out, int64_t ld_out, TileShape s) {
+    // s: tokens, the matrix's width, its rows
+    constexpr int TW = 4;
+    extern __shared__ __align__(16) char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 31, g = lane >> 5;
+    uint32_t tm, tn;
+    tile_of(s, (uint32_t(s.m) + 255) / 256, tm, tn);
+    const int m0 = min(int(tm) * 256, s.m - 256), c0 = int(tn) * 256;
+
+    const int64_t ld_b = ld_dy * 2;
+    const Buffer src = buffer_of(reinterpret_cast<const uint8_t *>(dy) + (m0 + 64 * wave) * ld_b);
+    const uint32_t off = uint32_t(lane >> 3) * uint32_t(ld_b) + 16 * ((lane & 7) ^ (lane >> 3));
+    const uint32_t offs[2] = {off, off ^ 16}, rows8 = 8 * uint32_t(ld_b);
+    Lds *to = (Lds *)smem + wave * 64 * 128;
+    auto copy = [&](int it, int buf, int i) {
+        copy16(src, offs[i & 1], uint32_t(it) * 128 + i * rows8, to + buf * 256 * 128 + i * 1024);
+    };
+    // columns past the last block's are not stored: any of the matrix's will do
+    const int group = tid & 31, octet = tid >> 5;
+    const int col = c0 + 8 * group < int(blocks_of_width(s.n)) * kBlock ? c0 + 8 * group : 0;
+    const uint8_t *wp = codes + int64_t(8 * octet) * ld_codes + col / 2;
+    const uint8_t *sp = scales + int64_t(8 * octet) * ld_scales + col / kBlock;
+    uint32_t word[8], top[8];
+    auto load = [&](int it) {
+        const uint8_t *w = wp + int64_t(it) * kStepHalf * ld_codes, *b = sp + int64_t(it) * kStepHalf * ld_scales;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            word[i] = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(w + i * ld_codes);
+            top[i] = b[i * ld_scales];
+        }
+    };
+    i32x4 *lds_w = reinterpret_cast<i32x4 *>(smem + 2 * 256 * 128);
+
+    f32x16 acc[TW][TW] = {};
+    const int wm = (wave & 1) * 128, wn = (wave >> 1) * 128;
+    const int turn = (r ^ (r >> 3 & 1)) & 7;
+    i32x4 q[2][TW], p[2][TW];
+    auto read = [&](int buf, int set, int j) {
+        const i32x4 *bx = reinterpret_cast<const i32x4 *>(smem + buf * 256 * 128), *bw = lds_w + buf * 256 * 8;
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+            q[set][t] = bx[(wm + 32 * t + r) * 8 + ((4 * g + j) ^ turn)];
+            p[set][t] = bw[place(wn + 32 * t + r, 4 * g + j)];
+        }
+    };
+    const int steps = s.k / kStepHalf, last = steps - 1;
+    auto run = [&](auto type) {
+        using T = decltype(type);
+        // columns 2 h and 2 h + 1 of the eight
+        auto store = [&](int buf, int h) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = uint32_t(widen_pair<T>(word[i], scale_operand(top[i]), h));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                i32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = int32_t(__builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], c ? 0x07060302u : 0x05040100u));
+                lds_w[buf * 256 * 8 + place(8 * group + 2 * h + c, octet)] = o;
+            }
+        };
+        auto multiply = [&](int set) {
+#pragma unroll
+            for (int j = 0; j < TW; ++j) {
+                i32x4 hi = q[set][j], lo;
+                if constexpr (!std::is_same_v<T, X>) split(q[set][j], hi, lo);
+#pragma unroll
+                for (int i = 0; i < TW; ++i) {
+                    acc[i][j] = mma32<T>(p[set][i], hi, acc[i][j]);
+                    if constexpr (!std::is_same_v<T, X>) acc[i][j] = mma32<T>(p[set][i], lo, acc[i][j]);
+                }
+            }
+        };
+        load(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) copy(0, 0, i);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) store(0, h);
+        __syncthreads();
+        load(min(1, last));
+        read(0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) copy(min(1, last), 1, i);
+        for (int it = 0; it < steps; ++it) {
+            const int P = it & 1, next = min(it + 1, last), second = min(it + 2, last);
+            __builtin_amdgcn_sched_barrier(0);
+            read(P, 1, 1);
+#pragma unroll
+            for (int i = 3; i < 8; ++i) copy(next, 1 - P, i);
+            multiply(0);
+            mix<1, 5>();
+            pin(acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read(P, 0, 2);
+            store(1 - P, 0);
+            store(1 - P, 1);
+            multiply(1);
+            pin(acc);
+            __builtin_amdgcn_sched_barrier(0);
+            read(P, 1, 3);
+            store(1 - P, 2);
+            store(1 - P, 3);
+            multiply(0);
+            pin(acc);
+            __builtin_amdgcn_sched_barrier(0);
+            __syncthreads();
+            load(second);
+            read(1 - P, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) copy(second, P, i);
+            multiply(1);
+            pin(acc);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if constexpr (std::is_same_v<X, f16>) {
+        // whether float16 holds the tile's columns: a thread looks at a block of every 32nd row
+        const int b = c0 / kBlock + (tid & 7);
+        bool fine = true;
+        if (b < int(blocks_of_width(s.n))) {
+#pragma unroll 8
+            for (int row = tid >> 3; row < s.k; row += 32) fine = fine && f16_scale(scales[int64_t(row) * ld_scales + b]);
+        }
+        if (__syncthreads_and(fine)) run(f16{});
+        else run(bf16{});
+    } else {
+        run(bf16{});
+    }
+    __syncthreads();  // no copy is on its way when the block ends
+    store_tile<TW>(acc, out, ld_out, m0 + wm, c0 + wn, s.m, s.n, lane);
+}
+
 }  // namespace vspmm
