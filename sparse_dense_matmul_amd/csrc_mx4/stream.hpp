@@ -40,15 +40,18 @@ __device__ __forceinline__ void pin(f32x16 (&acc)[A][B]) {
 // The order of a part of a step, 16 products: READS loads from LDS behind each of the first eight, so that they are
 // there at the next part's first product, and one of COPIES loads to LDS behind every other of the rest and then of all
 // (a wave waits to issue them while others' are on their way, its products with it).
-template <int READS, int COPIES>
+template <int READS, int COPIES, int LOADS = 0>
 __device__ __forceinline__ void mix() {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         if constexpr (READS > 0)
             if (i < 8) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
-        if constexpr (COPIES > 0)
+        if constexpr (LOADS > 0) {
+            if (i >= 8) __builtin_amdgcn_sched_group_barrier(0x010, LOADS, 0);
+        } else if constexpr (COPIES > 0) {
             if (i % 3 == 2 && i / 3 < COPIES) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        }
     }
 }
 
@@ -462,11 +465,12 @@ __global__ __launch_bounds__(256, 1) void k_stream_grad(const X *__restrict__ dy
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
             __syncthreads();
-            load(second);
             read(1 - P, 0, 0);
+            load(second);
 #pragma unroll
             for (int i = 0; i < 3; ++i) copy(second, P, i);
             multiply(1);
+            mix<1, 0, 3>();
             pin(acc);
             __builtin_amdgcn_sched_barrier(0);
         }
