@@ -87,8 +87,9 @@ vspmm_status zero_rows(O *out, int64_t ld, int64_t rows, int64_t width, hipStrea
 // Tiles of a product past one launch are of more than 2^43 results.
 bool too_many(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) / 64) > kI32Max; }
 
-// Up to this many tokens the few-token kernel, bound by the matrix's bytes; tiles beyond.
-constexpr int64_t kFewTokens = 64;
+// Up to this many tokens the few-token kernel, which reads the tokens once for 32 rows; tiles beyond (4,096 x 4,096:
+// 32 tokens 13 us by the one, 19 by the other, 64 tokens 21 and 18).
+constexpr int64_t kFewTokens = 32;
 
 template <typename X, typename O>
 void launch_few(Row<X> x, int64_t ld_x, int64_t ld_xs, const vspmm_mx4 &w, O *out, int64_t ld_out, int m, int n, int k,
@@ -102,34 +103,38 @@ void launch_few(Row<X> x, int64_t ld_x, int64_t ld_xs, const vspmm_mx4 &w, O *ou
     };
     using std::integral_constant;
     if (m <= 16) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    else if (m <= 32) go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-    else go(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+    else go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
 }
 
-// The tile's edge / 64: the largest whose tiles occupy the 256 compute units.
-int tile_width(int64_t m, int64_t n) {
-    for (int tw = 4; tw > 1; tw /= 2)
-        if (((m + 64 * tw - 1) / (64 * tw)) * ((n + 64 * tw - 1) / (64 * tw)) >= 224) return tw;
-    return 1;
-}
-
+// Tiles of 64 TW x 64 TW results by KS groups: the 128-wide ones, which read each operand half as often, where two to a
+// compute unit come together (2,000 tokens of 4,000 to 4,096 rows: 91 us, 137 with 64-wide ones); one with its steps
+// shared by two groups where there is one for each (1,000 tokens: 54, 62 with one group, 68); below that 64-wide ones,
+// shared by two groups (300: 31, 34 with one, 35 with four) or, where even they leave units idle, by four (128: 19, 21
+// with two, 27 with one).
 template <typename F>
 void with_tile(int64_t m, int64_t n, F &&f) {
-    switch (tile_width(m, n)) {
-        case 4: return f(std::integral_constant<int, 4>{});
-        case 2: return f(std::integral_constant<int, 2>{});
-        default: return f(std::integral_constant<int, 1>{});
-    }
+    using std::integral_constant;
+    constexpr integral_constant<int, 1> one{};
+    constexpr integral_constant<int, 2> two{};
+    constexpr integral_constant<int, 4> four{};
+    const int64_t wide = ((m + 127) / 128) * ((n + 127) / 128), narrow = ((m + 63) / 64) * ((n + 63) / 64);
+    if (wide >= 400) return f(two, one);
+    if (wide >= 192) return f(two, two);
+    if (narrow >= 256) return f(one, two);
+    return f(one, four);
+}
+
+// Whether tiles of 256 x 256 occupy the 256 compute units.
+bool fill(int64_t m, int64_t n) { return ((m + 255) / 256) * ((n + 255) / 256) >= 224; }
+
+bool streams(const void *x, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (ld & 7) == 0 && ld < (1 << 22);
 }
 
 bool streams(const vspmm_mx4 &a) {
     const auto bits = [](const void *p) { return reinterpret_cast<uintptr_t>(p); };
     return ((bits(a.codes) | a.ld_codes) & 15) == 0 && ((bits(a.scales) | a.ld_scales) & 3) == 0 &&
            a.ld_codes < (1 << 24) && a.ld_scales < (1 << 24);
-}
-
-bool streams(const void *x, int64_t ld) {
-    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (ld & 7) == 0 && ld < (1 << 22);
 }
 
 TileShape tile_shape(int64_t m, int64_t n, int64_t k, int edge, unsigned &tiles) {
@@ -211,7 +216,7 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
             launch_few(Row<T>{static_cast<const T *>(x)}, ld_x, 0, *w, o, ld_out, int(m), int(n), int(width), stream);
             return launched();
         }
-        if (m >= 256 && n >= 256 && width % kStepCodes == 0 && tile_width(m, n) == 4 && streams(x, ld_x) && streams(*w)) {
+        if (m >= 256 && n >= 256 && width % kChunkK == 0 && fill(m, n) && streams(x, ld_x) && streams(*w)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 256, tiles);
             allow_lds(reinterpret_cast<const void *>(&k_stream<T>), kStreamLds);
@@ -219,12 +224,12 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
                                w->codes, w->ld_codes, w->scales, w->ld_scales, o, ld_out, s);
             return launched();
         }
-        with_tile(m, n, [&](auto tw) {
-            constexpr int TW = decltype(tw)::value;
+        with_tile(m, n, [&](auto tw, auto ks) {
+            constexpr int TW = decltype(tw)::value, KS = decltype(ks)::value;
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 64 * TW, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_tile<TW, T, T>), tile_lds<TW>());
-            hipLaunchKernelGGL((k_tile<TW, T, T>), dim3(tiles), dim3(kTileThreads), tile_lds<TW>(), stream,
+            allow_lds(reinterpret_cast<const void *>(&k_tile<TW, KS, T, T>), KS * tile_lds<TW>());
+            hipLaunchKernelGGL((k_tile<TW, KS, T, T>), dim3(tiles), dim3(kTileThreads * KS), KS * tile_lds<TW>(), stream,
                                static_cast<const T *>(x), ld_x, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_out, s);
         });
@@ -244,7 +249,7 @@ vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t 
         using T = decltype(e);
         T *o = static_cast<T *>(grad);
         if (n == 0) return zero_rows(o, ld_grad, m, width, stream);
-        if (m >= 256 && n % kStepHalf == 0 && tile_width(m, width) == 4 && streams(dout, ld_dout)) {
+        if (m >= 256 && n % kStepHalf == 0 && fill(m, width) && streams(dout, ld_dout)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, width, n, 256, tiles);
             allow_lds(reinterpret_cast<const void *>(&k_stream_grad<T>), kStreamGradLds);
@@ -253,12 +258,12 @@ vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t 
                                ld_grad, s);
             return launched();
         }
-        with_tile(m, width, [&](auto tw) {
-            constexpr int TW = decltype(tw)::value;
+        with_tile(m, width, [&](auto tw, auto ks) {
+            constexpr int TW = decltype(tw)::value, KS = decltype(ks)::value;
             unsigned tiles;
             const TileShape s = tile_shape(m, width, n, 64 * TW, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_tile_grad<TW, T>), grad_lds<TW>());
-            hipLaunchKernelGGL((k_tile_grad<TW, T>), dim3(tiles), dim3(kTileThreads), grad_lds<TW>(), stream,
+            allow_lds(reinterpret_cast<const void *>(&k_tile_grad<TW, KS, T>), KS * grad_lds<TW>());
+            hipLaunchKernelGGL((k_tile_grad<TW, KS, T>), dim3(tiles), dim3(kTileThreads * KS), KS * grad_lds<TW>(), stream,
                                static_cast<const T *>(dout), ld_dout, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_grad, s);
         });
@@ -283,7 +288,7 @@ vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t w
                        int(width), stream);
             return launched();
         }
-        if (m >= 256 && n >= 256 && width % kStepCodes == 0 && tile_width(m, n) == 4 && streams(*x) && streams(*w)) {
+        if (m >= 256 && n >= 256 && width % kStepCodes == 0 && fill(m, n) && streams(*x) && streams(*w)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 256, tiles);
             allow_lds(reinterpret_cast<const void *>(&k_stream_both<T>), kStreamBothLds);
@@ -292,12 +297,12 @@ vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t w
                                ld_out, s);
             return launched();
         }
-        with_tile(m, n, [&](auto tw) {
-            constexpr int TW = decltype(tw)::value;
+        with_tile(m, n, [&](auto tw, auto ks) {
+            constexpr int TW = decltype(tw)::value, KS = decltype(ks)::value;
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 64 * TW, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_tile_both<TW, T>), both_lds<TW>());
-            hipLaunchKernelGGL((k_tile_both<TW, T>), dim3(tiles), dim3(kTileThreads), both_lds<TW>(), stream, x->codes,
+            allow_lds(reinterpret_cast<const void *>(&k_tile_both<TW, KS, T>), KS * both_lds<TW>());
+            hipLaunchKernelGGL((k_tile_both<TW, KS, T>), dim3(tiles), dim3(kTileThreads * KS), KS * both_lds<TW>(), stream, x->codes,
                                x->ld_codes, x->scales, x->ld_scales, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_out, s);
         });

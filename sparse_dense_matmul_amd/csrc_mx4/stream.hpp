@@ -13,9 +13,9 @@ using Buffer = __amdgpu_buffer_rsrc_t;
 __device__ __forceinline__ Buffer buffer_of(const uint8_t *p, uint32_t bytes = 0x80000000u) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(p), 0, int(bytes), 0x00020000);
 }
-// Rows of scales from row0 on: 16 bytes are copied where a row's last 8 are left, and past the last row are zeros.
-__device__ __forceinline__ Buffer scales_of(const uint8_t *p, int64_t ld, int row0, int rows, int blocks) {
-    const int64_t bytes = int64_t(rows - 1 - row0) * ld + blocks;
+// Rows of `width` bytes from row0 on whose copies run past a row's end: past the last row's are zeros.
+__device__ __forceinline__ Buffer rows_of(const uint8_t *p, int64_t ld, int row0, int rows, int width) {
+    const int64_t bytes = int64_t(rows - 1 - row0) * ld + width;
     return buffer_of(p + row0 * ld, bytes < 0x80000000ll ? uint32_t(bytes) : 0x80000000u);
 }
 __device__ __forceinline__ void copy16(Buffer from, uint32_t offset, uint32_t more, Lds *to) {
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256, 1) void k_stream_both(const uint8_t *__restric
     };
     // scales go by two steps, 16 bytes a row: in each of the two a wave copies those of 64 of its 128 rows
     const int64_t lds_ = mine ? ld_xs : ld_scales;
-    const Buffer src_s = scales_of(mine ? x_scales : scales, lds_, row0, mine ? s.m : s.n, s.k / kBlock);
+    const Buffer src_s = rows_of(mine ? x_scales : scales, lds_, row0, mine ? s.m : s.n, s.k / kBlock);
     const uint32_t off_s = uint32_t(lane) * uint32_t(lds_), rows64 = 64 * uint32_t(lds_);
     const char *tops = smem + 2 * 512 * 128;
     Lds *to_s = (Lds *)tops + wave * 128 * 16;
@@ -217,8 +217,8 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
     const char *lds_x = smem, *lds_w = smem + 2 * 256 * 128, *lds_s = smem + 4 * 256 * 128;
     const int64_t ld_xb = ld_x * 2;
     const Buffer src_x = buffer_of(reinterpret_cast<const uint8_t *>(x) + (m0 + 64 * wave) * ld_xb);
-    const Buffer src_w = buffer_of(codes + (n0 + 64 * wave) * ld_codes);
-    const Buffer src_s = scales_of(scales, ld_scales, n0 + 64 * wave, s.n, s.k / kBlock);
+    const Buffer src_w = rows_of(codes, ld_codes, n0 + 64 * wave, s.n, s.k / 2);
+    const Buffer src_s = rows_of(scales, ld_scales, n0 + 64 * wave, s.n, s.k / kBlock);
     const uint32_t piece = 16 * ((lane & 7) ^ (lane >> 3));
     const uint32_t off_x = uint32_t(lane >> 3) * uint32_t(ld_xb), off_w = uint32_t(lane >> 3) * uint32_t(ld_codes);
     const uint32_t offs_x[2] = {off_x + piece, off_x + (piece ^ 16)}, offs_w[2] = {off_w + piece, off_w + (piece ^ 16)};
@@ -331,11 +331,11 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
         // whether float16 holds the tile's rows: a thread looks at one row's scales
         const uint8_t *row = scales + int64_t(n0 + int(threadIdx.x)) * ld_scales;
         bool fine = true;
-        for (int i = 0; i < s.k / kBlock; i += 8) {
-            using Byte8 = int32_t __attribute__((ext_vector_type(2), aligned(1)));
-            const Byte8 v = *reinterpret_cast<const Byte8 *>(row + i);
+#pragma unroll 8
+        for (int i = 0; i < s.k / kBlock; i += 4) {
+            const uint32_t v = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(row + i);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) fine = fine && f16_scale(uint32_t(v[e / 4]) >> (8 * (e & 3)) & 255);
+            for (int e = 0; e < 4; ++e) fine = fine && f16_scale(v >> (8 * e) & 255);
         }
         if (__syncthreads_and(fine)) run(f16{});
         else run(bf16{});

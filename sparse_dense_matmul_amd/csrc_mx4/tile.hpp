@@ -23,16 +23,71 @@ constexpr int kStepCodes = 256;  // codes of a step of 4-bit rows
 __device__ __forceinline__ int spread(int row) { return (row ^ (row >> 3)) & 7; }
 __device__ __forceinline__ int place(int row, int chunk) { return row * 8 + (chunk ^ spread(row)); }
 
-// Eight 16-bit values at k of a row, those from the width on as zeros. `whole`: none are.
-__device__ __forceinline__ i32x4 load_chunk(const uint16_t *row, int k, int width, bool whole) {
-    if (whole) return *reinterpret_cast<const Half16 *>(row + k);
-    return load_half(row, k, width);
-}
-
 struct TileShape {
     int m, n, k;            // tokens, rows and the contraction's length
     uint32_t tiles_n;       // tiles along n
 };
+
+// A block is KS groups of four waves, each over a part of the contraction's steps with buffers of its own.
+__device__ __forceinline__ int group_thread() { return int(threadIdx.x) & (kTileThreads - 1); }
+__device__ __forceinline__ int group_number() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kTileThreads); }
+
+// A barrier for what lies in LDS: loads to registers stay on their way (__syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Steps [first, first + steps) of a group: load(step) to registers, store(buffer) from there to LDS, compute(buffer). A
+// step is loaded before the barrier that opens the one before it.
+template <typename Load, typename Store, typename Compute>
+__device__ __forceinline__ void run_steps(int first, int steps, Load &&load, Store &&store, Compute &&compute) {
+    load(first);
+    store(0);
+    load(first + 1);
+    lds_barrier();
+    for (int it = 0; it < steps; ++it) {
+        compute(it & 1);
+        store((it + 1) & 1);
+        load(first + it + 2);
+        lds_barrier();
+    }
+}
+
+// The groups' sums added up in the first, in order, through LDS that nothing else uses any more.
+template <int KS, int TW>
+__device__ __forceinline__ void join_groups(f32x16 (&acc)[TW][TW], char *smem) {
+    if constexpr (KS > 1) {
+        f32x4 *parts = reinterpret_cast<f32x4 *>(smem);  // [wave][4 TW][lane] of a group at a time
+        const int tid = group_thread(), group = group_number();
+#pragma unroll 1
+        for (int k = 1; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < TW; ++i) {
+                __syncthreads();
+                if (group == k) {
+#pragma unroll
+                    for (int j = 0; j < TW; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            parts[(j * 4 + e) * kTileThreads + tid] =
+                                f32x4{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+                }
+                __syncthreads();
+                if (group == 0) {
+#pragma unroll
+                    for (int j = 0; j < TW; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const f32x4 v = parts[(j * 4 + e) * kTileThreads + tid];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) acc[i][j][4 * e + c] += v[c];
+                        }
+                }
+            }
+    }
+}
 
 // Consecutive blocks go to the eight chiplets in turn; each chiplet takes a run of tiles, down strips of 8 tiles of
 // tokens, so that what its L2 holds is used by neighbours.
@@ -54,21 +109,26 @@ struct Tokens {
     int chunk;
 
     __device__ __forceinline__ void init(const void *x, int64_t ld, int m0, int m) {
-        chunk = threadIdx.x & 7;
+        chunk = group_thread() & 7;
 #pragma unroll
         for (int i = 0; i < 2 * TW; ++i) {
-            const int r = m0 + i * 32 + int(threadIdx.x >> 3);
+            const int r = m0 + i * 32 + (group_thread() >> 3);
             row[i] = static_cast<const uint16_t *>(x) + int64_t(r < m ? r : m - 1) * ld;
         }
     }
     __device__ __forceinline__ void load(int k0, int width) {
-        const bool whole = k0 + kStepHalf <= width;
+        const int k = k0 + 8 * chunk;
+        if (k0 + kStepHalf <= width) {
 #pragma unroll
-        for (int i = 0; i < 2 * TW; ++i) v[i] = load_chunk(row[i], k0 + 8 * chunk, width, whole);
+            for (int i = 0; i < 2 * TW; ++i) v[i] = *reinterpret_cast<const Half16 *>(row[i] + k);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * TW; ++i) v[i] = load_half(row[i], k, width);
+        }
     }
     __device__ __forceinline__ void store(i32x4 *lds) const {
 #pragma unroll
-        for (int i = 0; i < 2 * TW; ++i) lds[place(i * 32 + int(threadIdx.x >> 3), chunk)] = v[i];
+        for (int i = 0; i < 2 * TW; ++i) lds[place(i * 32 + (group_thread() >> 3), chunk)] = v[i];
     }
 };
 
@@ -83,14 +143,14 @@ struct Codes {
 
     __device__ __forceinline__ void init(const uint8_t *codes, int64_t ld, const uint8_t *scales, int64_t ld_scales,
                                          int r0, int rows, int width) {
-        chunk = threadIdx.x & 7;
+        chunk = group_thread() & 7;
         blocks = int(blocks_of_width(width));
 #pragma unroll
         for (int i = 0; i < 2 * TW; ++i) {
-            const int r = r0 + i * 32 + int(threadIdx.x >> 3);
+            const int r = r0 + i * 32 + (group_thread() >> 3);
             row[i] = codes + int64_t(r < rows ? r : rows - 1) * ld;
         }
-        const int r = r0 + int(threadIdx.x);
+        const int r = r0 + group_thread();
         tops = scales + int64_t(r < rows ? r : rows - 1) * ld_scales;
     }
     __device__ __forceinline__ void load(int b0) {
@@ -98,7 +158,7 @@ struct Codes {
 #pragma unroll
         for (int i = 0; i < 2 * TW; ++i)
             v[i] = here ? *reinterpret_cast<const Byte16 *>(row[i] + int64_t(b0 + chunk) * kBlockBytes) : i32x4{};
-        if (int(threadIdx.x) >= kEdge) return;
+        if (group_thread() >= kEdge) return;
         if (b0 + 8 <= blocks) {
             using Two = uint32_t __attribute__((ext_vector_type(2), aligned(1)));
             const Two t = *reinterpret_cast<const Two *>(tops + b0);
@@ -112,8 +172,8 @@ struct Codes {
     }
     __device__ __forceinline__ void store(i32x4 *lds, uint2 *lds_s) const {
 #pragma unroll
-        for (int i = 0; i < 2 * TW; ++i) lds[place(i * 32 + int(threadIdx.x >> 3), chunk)] = v[i];
-        if (int(threadIdx.x) < kEdge) lds_s[threadIdx.x] = make_uint2(s[0], s[1]);
+        for (int i = 0; i < 2 * TW; ++i) lds[place(i * 32 + (group_thread() >> 3), chunk)] = v[i];
+        if (group_thread() < kEdge) lds_s[group_thread()] = make_uint2(s[0], s[1]);
     }
 };
 
@@ -174,18 +234,18 @@ constexpr size_t tile_lds() {  // bytes: two buffers of tokens, codes and scales
     return size_t(2) * 64 * TW * (128 + 32 + 2);
 }
 
-template <int TW, typename X, typename O>
-__global__ __launch_bounds__(kTileThreads) void k_tile(const X *__restrict__ x, int64_t ld_x,
+template <int TW, int KS, typename X, typename O>
+__global__ __launch_bounds__(kTileThreads *KS) void k_tile(const X *__restrict__ x, int64_t ld_x,
                                                        const uint8_t *__restrict__ codes, int64_t ld_codes,
                                                        const uint8_t *__restrict__ scales, int64_t ld_scales,
                                                        O *__restrict__ out, int64_t ld_out, TileShape s) {
     constexpr int EDGE = 64 * TW, SLOTS = EDGE * 2;  // 16-byte blocks of codes of a step
     constexpr int OWN = SLOTS / kTileThreads > 0 ? SLOTS / kTileThreads : 1;
     extern __shared__ __align__(16) char smem[];
-    i32x4 *lds_x = reinterpret_cast<i32x4 *>(smem);
+    i32x4 *lds_x = reinterpret_cast<i32x4 *>(smem + group_number() * tile_lds<TW>());
     i32x4 *lds_w = lds_x + 2 * EDGE * 8;
     uint16_t *lds_s = reinterpret_cast<uint16_t *>(lds_w + 2 * SLOTS);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = group_thread(), lane = tid & 63, wave = tid >> 6;
     const int r = lane & 31, g = lane >> 5;
     uint32_t tm, tn;
     tile_of(s, (uint32_t(s.m) + EDGE - 1) / EDGE, tm, tn);
@@ -196,7 +256,7 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(const X *__restrict__ x, 
     tok.init(x, ld_x, m0, s.m);
     const uint8_t *wrow[OWN], *srow;
     i32x4 wv[OWN];
-    uint32_t sv = 0;
+    uint32_t sv;
 #pragma unroll
     for (int i = 0; i < OWN; ++i) {
         const int slot = i * kTileThreads + tid;  // [row / 32][block][row % 32]
@@ -215,12 +275,14 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(const X *__restrict__ x, 
         if (own_w) {
 #pragma unroll
             for (int i = 0; i < OWN; ++i)
-                wv[i] = b + wb < blocks ? *reinterpret_cast<const Byte16 *>(wrow[i] + int64_t(b + wb) * kBlockBytes)
-                                        : i32x4{};
+                wv[i] = b + wb < blocks
+                               ? *reinterpret_cast<const Byte16 *>(wrow[i] + int64_t(b + wb) * kBlockBytes)
+                               : i32x4{};
         }
         if (own_s) {
-            sv = srow[b];
-            sv |= (b + 1 < blocks ? uint32_t(srow[b + 1]) : 127u) << 8;
+            // in one load: joining two would wait for them here
+            if (b + 2 <= blocks) sv = *reinterpret_cast<const uint16_t __attribute__((aligned(1))) *>(srow + b);
+            else sv = (b < blocks ? uint32_t(srow[b]) : 127u) | 127u << 8;
         }
     };
     auto store = [&](int buf) {
@@ -268,17 +330,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile(const X *__restrict__ x, 
         }
     };
 
-    const int steps = (s.k + kStepHalf - 1) / kStepHalf;
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int it = 0; it < steps; ++it) {
-        const bool more = it + 1 < steps;
-        if (more) load(it + 1);
-        compute(it & 1);
-        if (more) store((it + 1) & 1);
-        __syncthreads();
-    }
+    // each group has as many steps as the first: those past the end are zeros
+    const int all = (s.k + kStepHalf - 1) / kStepHalf, steps = (all + KS - 1) / KS, first = group_number() * steps;
+    run_steps(first, steps, load, store, compute);
+    join_groups<KS>(acc, smem);
+    if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
 }
 
@@ -293,8 +349,8 @@ constexpr size_t grad_lds() {  // bytes: two buffers of the gradient's rows and 
 // (which holds every value) on their way to LDS: a thread takes eight columns of eight rows n, a word of codes from
 // each, and pairs of rows joined make each column's eight values 16 bytes of its LDS row. float16 gradients meet them
 // in two bfloat16 parts.
-template <int TW, typename X>
-__global__ __launch_bounds__(kTileThreads) void k_tile_grad(const X *__restrict__ dy, int64_t ld_dy,
+template <int TW, int KS, typename X>
+__global__ __launch_bounds__(kTileThreads *KS) void k_tile_grad(const X *__restrict__ dy, int64_t ld_dy,
                                                             const uint8_t *__restrict__ codes, int64_t ld_codes,
                                                             const uint8_t *__restrict__ scales, int64_t ld_scales,
                                                             X *__restrict__ out, int64_t ld_out, TileShape s) {
@@ -302,9 +358,9 @@ __global__ __launch_bounds__(kTileThreads) void k_tile_grad(const X *__restrict_
     constexpr int EDGE = 64 * TW;
     constexpr int GROUPS = EDGE / 8;  // groups of eight columns
     extern __shared__ __align__(16) char smem[];
-    i32x4 *lds_x = reinterpret_cast<i32x4 *>(smem);
+    i32x4 *lds_x = reinterpret_cast<i32x4 *>(smem + group_number() * grad_lds<TW>());
     i32x4 *lds_w = lds_x + 2 * EDGE * 8;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = group_thread(), lane = tid & 63, wave = tid >> 6;
     const int r = lane & 31, g = lane >> 5;
     uint32_t tm, tn;
     tile_of(s, (uint32_t(s.m) + EDGE - 1) / EDGE, tm, tn);
@@ -318,18 +374,28 @@ __global__ __launch_bounds__(kTileThreads) void k_tile_grad(const X *__restrict_
     const int blocks = int(blocks_of_width(s.n));
     const int col = c0 + 8 * group < blocks * kBlock ? c0 + 8 * group : 0;
     const uint8_t *wp = codes + col / 2, *sp = scales + col / kBlock;
-    uint32_t word[8];
-    uint32_t top[8];
+    uint32_t word[8], top[8];
     auto load = [&](int it) {
         tok.load(it * kStepHalf, s.k);
         if (!own) return;
         const int row0 = it * kStepHalf + 8 * octet;
+        const uint8_t *w = wp + row0 * ld_codes, *b = sp + row0 * ld_scales;
+        if (row0 + 8 <= s.k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int row = row0 + i;
-            const bool here = row < s.k;
-            word[i] = here ? *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(wp + row * ld_codes) : 0;
-            top[i] = here ? sp[row * ld_scales] : 127;
+            for (int i = 0; i < 8; ++i) {
+                word[i] = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(w + i * ld_codes);
+                top[i] = b[i * ld_scales];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                word[i] = 0;
+                top[i] = 127;
+                if (row0 + i < s.k) {
+                    word[i] = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(w + i * ld_codes);
+                    top[i] = b[i * ld_scales];
+                }
+            }
         }
     };
     auto store = [&](int buf) {
@@ -364,17 +430,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile_grad(const X *__restrict_
         }
     };
 
-    const int steps = (s.k + kStepHalf - 1) / kStepHalf;
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int it = 0; it < steps; ++it) {
-        const bool more = it + 1 < steps;
-        if (more) load(it + 1);
-        compute(it & 1);
-        if (more) store((it + 1) & 1);
-        __syncthreads();
-    }
+    // each group has as many steps as the first: those past the end are zeros
+    const int all = (s.k + kStepHalf - 1) / kStepHalf, steps = (all + KS - 1) / KS, first = group_number() * steps;
+    run_steps(first, steps, load, store, compute);
+    join_groups<KS>(acc, smem);
+    if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, c0 + wn, s.m, s.n, lane);
 }
 
@@ -385,19 +445,19 @@ constexpr size_t both_lds() {  // bytes: two buffers of both sides' codes and sc
     return size_t(2) * 64 * TW * 2 * (128 + 8);
 }
 
-template <int TW, typename O>
-__global__ __launch_bounds__(kTileThreads) void k_tile_both(const uint8_t *__restrict__ x_codes, int64_t ld_x,
+template <int TW, int KS, typename O>
+__global__ __launch_bounds__(kTileThreads *KS) void k_tile_both(const uint8_t *__restrict__ x_codes, int64_t ld_x,
                                                             const uint8_t *__restrict__ x_scales, int64_t ld_xs,
                                                             const uint8_t *__restrict__ codes, int64_t ld_codes,
                                                             const uint8_t *__restrict__ scales, int64_t ld_scales,
                                                             O *__restrict__ out, int64_t ld_out, TileShape s) {
     constexpr int EDGE = 64 * TW;
     extern __shared__ __align__(16) char smem[];
-    i32x4 *lds_x = reinterpret_cast<i32x4 *>(smem);
+    i32x4 *lds_x = reinterpret_cast<i32x4 *>(smem + group_number() * both_lds<TW>());
     i32x4 *lds_w = lds_x + 2 * EDGE * 8;
     uint2 *lds_xs = reinterpret_cast<uint2 *>(lds_w + 2 * EDGE * 8);
     uint2 *lds_ws = lds_xs + 2 * EDGE;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = group_thread() & 63, wave = group_thread() >> 6;
     const int r = lane & 31, g = lane >> 5;
     uint32_t tm, tn;
     tile_of(s, (uint32_t(s.m) + EDGE - 1) / EDGE, tm, tn);
@@ -446,17 +506,11 @@ __global__ __launch_bounds__(kTileThreads) void k_tile_both(const uint8_t *__res
         part(std::integral_constant<int, 3>{});
     };
 
-    const int steps = (s.k + kStepCodes - 1) / kStepCodes;
-    load(0);
-    store(0);
-    __syncthreads();
-    for (int it = 0; it < steps; ++it) {
-        const bool more = it + 1 < steps;
-        if (more) load(it + 1);
-        compute(it & 1);
-        if (more) store((it + 1) & 1);
-        __syncthreads();
-    }
+    // each group has as many steps as the first: those past the end are zeros
+    const int all = (s.k + kStepCodes - 1) / kStepCodes, steps = (all + KS - 1) / KS, first = group_number() * steps;
+    run_steps(first, steps, load, store, compute);
+    join_groups<KS>(acc, smem);
+    if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
 }
 
