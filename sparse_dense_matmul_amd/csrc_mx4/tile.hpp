@@ -345,10 +345,10 @@ constexpr size_t grad_lds() {  // bytes: two buffers of the gradient's rows and 
     return size_t(2) * 64 * TW * 256;
 }
 
-// dx[m][c] = sum over n of dy[m][n] w[n][c]: the matrix's columns c are the rows of the tile, widened to bfloat16
-// (which holds every value) on their way to LDS: a thread takes eight columns of eight rows n, a word of codes from
-// each, and pairs of rows joined make each column's eight values 16 bytes of its LDS row. float16 gradients meet them
-// in two bfloat16 parts.
+// dx[m][c] = sum over n of dy[m][n] w[n][c]: the matrix's columns c are the rows of the tile, widened on their
+// way to LDS: a thread takes eight columns of eight rows n, a word of codes from each, and pairs of rows joined make each
+// column's eight values 16 bytes of its LDS row. float16 gradients meet them in float16 where it holds the tile's
+// columns, else, in two bfloat16 parts, in bfloat16, which holds every value.
 template <int TW, int KS, typename X>
 __global__ __launch_bounds__(kTileThreads *KS) void k_tile_grad(const X *__restrict__ dy, int64_t ld_dy,
                                                             const uint8_t *__restrict__ codes, int64_t ld_codes,
@@ -398,41 +398,56 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile_grad(const X *__restr
             }
         }
     };
-    auto store = [&](int buf) {
-        tok.store(lds_x + buf * EDGE * 8);
-        if (!own) return;
-        i32x4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = widen<bf16>(word[i], scale_operand(top[i]));
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            i32x4 o;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                o[i] = int32_t(__builtin_amdgcn_perm(uint32_t(v[2 * i + 1][c / 2]), uint32_t(v[2 * i][c / 2]),
-                                                     c & 1 ? 0x07060302u : 0x05040100u));
-            lds_w[buf * EDGE * 8 + place(8 * group + c, octet)] = o;
-        }
-    };
-
     f32x16 acc[TW][TW] = {};
     const int wm = (wave & 1) * 32 * TW, wn = (wave >> 1) * 32 * TW;
-    auto compute = [&](int buf) {
-        const i32x4 *bx = lds_x + buf * EDGE * 8, *bw = lds_w + buf * EDGE * 8;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            i32x4 p[TW], q[TW];
-#pragma unroll
-            for (int t = 0; t < TW; ++t) q[t] = bx[place(wm + 32 * t + r, 4 * g + j)];
-#pragma unroll
-            for (int t = 0; t < TW; ++t) p[t] = bw[place(wn + 32 * t + r, 4 * g + j)];
-            multiply_tiles<bf16, std::is_same_v<X, f16>, TW>(acc, p, q);
-        }
-    };
-
     // each group has as many steps as the first: those past the end are zeros
     const int all = (s.k + kStepHalf - 1) / kStepHalf, steps = (all + KS - 1) / KS, first = group_number() * steps;
-    run_steps(first, steps, load, store, compute);
+    auto run = [&](auto type) {
+        using T = decltype(type);
+        auto store = [&](int buf) {
+            tok.store(lds_x + buf * EDGE * 8);
+            if (!own) return;
+            i32x4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = widen<T>(word[i], scale_operand(top[i]));
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                i32x4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[i] = int32_t(__builtin_amdgcn_perm(uint32_t(v[2 * i + 1][c / 2]), uint32_t(v[2 * i][c / 2]),
+                                                         c & 1 ? 0x07060302u : 0x05040100u));
+                lds_w[buf * EDGE * 8 + place(8 * group + c, octet)] = o;
+            }
+        };
+        auto compute = [&](int buf) {
+            const i32x4 *bx = lds_x + buf * EDGE * 8, *bw = lds_w + buf * EDGE * 8;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                i32x4 p[TW], q[TW];
+#pragma unroll
+                for (int t = 0; t < TW; ++t) q[t] = bx[place(wm + 32 * t + r, 4 * g + j)];
+#pragma unroll
+                for (int t = 0; t < TW; ++t) p[t] = bw[place(wn + 32 * t + r, 4 * g + j)];
+                multiply_tiles<T, !std::is_same_v<T, X>, TW>(acc, p, q);
+            }
+        };
+        run_steps(first, steps, load, store, compute);
+    };
+    if constexpr (std::is_same_v<X, f16>) {
+        // whether float16 holds the tile's columns: the block's threads share their scales
+        constexpr int TOPS = EDGE / kBlock;
+        bool fine = true;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < int64_t(s.k) * TOPS; i += kTileThreads * KS) {
+            const int b = c0 / kBlock + int(i % TOPS);
+            fine = fine && (b >= blocks || f16_scale(scales[i / TOPS * ld_scales + b]));
+        }
+        if (__syncthreads_and(fine)) run(f16{});
+        else run(bf16{});
+    } else {
+        run(bf16{});
+    }
     join_groups<KS>(acc, smem);
     if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, c0 + wn, s.m, s.n, lane);
