@@ -23,7 +23,8 @@ namespace {
 constexpr int kTokensMax = 1024;
 constexpr int kExpertsMax = 4096;
 constexpr int kUpWaves = 8;     // of a block of the first launch
-constexpr int kDownWaves = 16;  // of a block of the second
+constexpr int kDownWaves = 8;  // of a block of the second
+constexpr size_t kStageMax = 48 * 1024;  // bytes of staged tokens that leave room for two blocks
 
 // ------------------------------------------------------------------ kernels
 
@@ -38,16 +39,53 @@ struct Choices {
     }
 };
 
-// Between the launches: how many experts are in use, which, the tokens sent to each in order with a slot of each (a
-// token sent twice to an expert is listed once, with both weights), where the list passes each multiple of kGroup
-// tokens, and the hidden values by slot, in whole chunks with zeros at the end.
-constexpr int kGroup = 128, kGroups = kTokensMax / kGroup;
+// Between the launches: how many experts are in use, which, how many of each group of kGroup tokens are sent to each and
+// which, in order, with a slot of each (a token sent twice to an expert is listed once, with both weights), and the
+// hidden values by slot, in whole chunks with zeros at the end. With few choices the second launch finds all but the
+// hidden values by itself.
+constexpr int kGroup = 128;
 struct Between {
     int *count, *expert;  // [1], [most]
-    int *bounds;          // [most, kGroups + 1]
-    int2 *list;           // [most, tokens]: token, slot
+    int *counts;          // [most, groups]
+    int2 *list;           // [most, groups, kGroup]: token, slot
     bf16 *hi, *lo;        // [slots, padded]
     int64_t padded;
+    int groups;
+};
+
+// Up to 64 choices of up to 16 tokens: a wave holds them all, one a lane, and finds the experts in use, in order of
+// their first choice, and an expert's tokens by ballots.
+struct Few {
+    int expert;      // the lane's choice, -1: none
+    float weight;    // and its weight
+    uint64_t first;  // the lanes whose expert none before has chosen
+    int top_k;
+
+    __device__ __forceinline__ Few(const Choices &ch, int lane) : expert(-1), weight(0.0f), top_k(ch.top_k) {
+        const int slots = ch.tokens * ch.top_k;
+        if (lane < slots) expert = ch.expert(lane), weight = ch.weights[lane];
+        bool again = expert < 0;
+        for (int s = 0; s < slots; ++s) again = again || (lane > s && expert == __builtin_amdgcn_readlane(expert, s));
+        first = __ballot(!again);
+    }
+    __device__ __forceinline__ int count() const { return __popcll(first); }
+    // the a-th expert in use
+    __device__ __forceinline__ int number(int a) const {
+        uint64_t m = first;
+        for (; a > 0; --a) m &= m - 1;
+        return __builtin_amdgcn_readlane(expert, __builtin_ctzll(m));
+    }
+    // how many tokens expert e has; in lane r its r-th token and that one's choices of it, as bits from the first on
+    __device__ __forceinline__ int tokens(int e, int lane, int &token, uint64_t &choices) const {
+        const uint64_t all = __ballot(expert == e);
+        const uint64_t own = top_k < 64 ? (uint64_t(1) << top_k) - 1 : ~uint64_t(0);
+        const bool has = lane * top_k < 64 && (all >> (lane * top_k) & own) != 0;
+        const uint64_t here = __ballot(has);
+        const int rank = __popcll(here & ((uint64_t(1) << lane) - 1));
+        token = __builtin_amdgcn_ds_permute((has ? rank : 63) * 4, lane);  // lane 63 has no token of 16
+        choices = lane < __popcll(here) ? all >> (token * top_k) & own : 0;
+        return __popcll(here);
+    }
 };
 
 template <typename T>
@@ -71,17 +109,45 @@ __device__ __forceinline__ float activate(float g) {
     else return g / (1.0f + expf(-g));
 }
 
+// The hidden values of 16 units of the weights' rows f0 .. for a tile of 16 tokens from the waves' parts, by one wave:
+// lane (r, g) has token r's units f0 + 4 g .. + 3.
+template <bool GELU, int WAVES>
+__device__ __forceinline__ void store_hidden(const f32x4 (&parts)[WAVES][2][64], int lane, int f0, int hidden, bool last,
+                                             int slot, float weight, const Between &to) {
+    f32x4 sg = parts[0][0][lane], su = parts[0][1][lane];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) sg += parts[v][0][lane], su += parts[v][1][lane];
+    const int f = f0 + 4 * (lane >> 4);
+    const int64_t base = slot * to.padded + f;
+    bf16x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float h = f + i < hidden ? weight * (activate<GELU>(sg[i]) * su[i]) : 0.0f;
+        hi[i] = bf16(h);
+        // an infinity has no second part
+        lo[i] = __builtin_isinf(float(hi[i])) ? bf16(0.0f) : bf16(h - float(hi[i]));
+    }
+    *reinterpret_cast<bf16x4 *>(to.hi + base) = hi;
+    *reinterpret_cast<bf16x4 *>(to.lo + base) = lo;
+    if (last)  // zeros to the end of the last chunk
+        for (int64_t i = 16; f + i < to.padded; i += 16) {
+            *reinterpret_cast<bf16x4 *>(to.hi + base + i) = bf16x4{};
+            *reinterpret_cast<bf16x4 *>(to.lo + base + i) = bf16x4{};
+        }
+}
+
+// A block takes `own` runs of 16 hidden units of one expert, its waves an eighth of the contraction each.
 template <typename W, typename X, bool GELU, int MT>
 __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const X *__restrict__ x, int64_t ld_x,
                                                               Matrix<W> gate, Matrix<W> up, int width, int hidden,
-                                                              Between to) {
+                                                              int own, Between to) {
     __shared__ uint32_t used[kExpertsMax / 32];
     __shared__ int s_expert, s_total, s_counts[kTokensMax / 64];
     __shared__ int s_slot[kTokensMax];
     __shared__ float s_weight[kTokensMax];
     __shared__ uint16_t s_token[kTokensMax];
-    __shared__ f32x4 parts[kUpWaves][2][64];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ f32x4 parts[2][kUpWaves][2][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slots = ch.tokens * ch.top_k, a = blockIdx.y;
 
     // the experts in use as bits, and the a-th of them
@@ -95,16 +161,16 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
     __syncthreads();
     if (wave == 0) {
         const uint32_t w0 = 2 * lane < words ? used[2 * lane] : 0, w1 = 2 * lane + 1 < words ? used[2 * lane + 1] : 0;
-        const int own = __popc(w0) + __popc(w1);
-        int before = own;
+        const int own_bits = __popc(w0) + __popc(w1);
+        int before = own_bits;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
             const int t = __shfl_up(before, d);
             if (lane >= d) before += t;
         }
         if (lane == 63) s_total = before;
-        before -= own;
-        if (a >= before && a < before + own) {
+        before -= own_bits;
+        if (a >= before && a < before + own_bits) {
             int left = a - before, at = 64 * lane;
             uint32_t w = w0;
             if (left >= __popc(w0)) left -= __popc(w0), at += 32, w = w1;
@@ -118,12 +184,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
     const int e = s_expert;
 
     // its tokens in order, each with its first slot here and the sum of its weights
-    constexpr int GROUPS = kTokensMax / 64 / kUpWaves;
-    int slot[GROUPS];
-    float weight[GROUPS];
-    uint64_t here[GROUPS];
+    constexpr int RUNS = kTokensMax / 64 / kUpWaves;
+    int slot[RUNS];
+    float weight[RUNS];
+    uint64_t here[RUNS];
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
+    for (int i = 0; i < RUNS; ++i) {
         const int t = (i * kUpWaves + wave) * 64 + lane;
         slot[i] = -1;
         weight[i] = 0.0f;
@@ -138,144 +204,227 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
         here[i] = __ballot(slot[i] >= 0);
         if (lane == 0) s_counts[i * kUpWaves + wave] = __popcll(here[i]);
     }
-    if (blockIdx.x == 0 && tid == 0) to.expert[a] = e;
     __syncthreads();
+    const bool list = blockIdx.x == 0;  // this block writes the expert's list
+    if (list && tid == 0) to.expert[a] = e;
+    if (list && tid < to.groups)
+        to.counts[int64_t(a) * to.groups + tid] = s_counts[2 * tid] + s_counts[2 * tid + 1];
     int mine = 0;
 #pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
+    for (int i = 0; i < RUNS; ++i) {
+        const int run = i * kUpWaves + wave;
         int at = 0;
-        for (int c = 0; c < i * kUpWaves + wave; ++c) at += s_counts[c];
-        const int group = i * kUpWaves + wave;
-        if (blockIdx.x == 0 && lane == 0 && group % (kGroup / 64) == 0)
-            to.bounds[int64_t(a) * (kGroups + 1) + group / (kGroup / 64)] = at;
+        for (int c = 0; c < run; ++c) at += s_counts[c];
         if (slot[i] >= 0) {
-            at += __popcll(here[i] & ((uint64_t(1) << lane) - 1));
-            s_token[at] = uint16_t(group * 64 + lane);
-            s_slot[at] = slot[i];
-            s_weight[at] = weight[i];
-            if (blockIdx.x == 0) to.list[int64_t(a) * ch.tokens + at] = make_int2(group * 64 + lane, slot[i]);
+            const int rank = __popcll(here[i] & ((uint64_t(1) << lane) - 1));
+            s_token[at + rank] = uint16_t(run * 64 + lane);
+            s_slot[at + rank] = slot[i];
+            s_weight[at + rank] = weight[i];
+            if (list)
+                to.list[(int64_t(a) * to.groups + run / 2) * kGroup + rank + (run & 1 ? s_counts[run - 1] : 0)] =
+                    make_int2(run * 64 + lane, slot[i]);
         }
     }
     for (int c = 0; c < kTokensMax / 64; ++c) mine += s_counts[c];
-    if (blockIdx.x == 0 && tid == 0) to.bounds[int64_t(a) * (kGroups + 1) + kGroups] = mine;
     __syncthreads();
 
     const int r = lane & 15, g = lane >> 4;
-    const int f0 = int(blockIdx.x) * 16, f = min(f0 + r, hidden - 1);
-    const Row<W> rows[2] = {gate.row(e, f), up.row(e, f)};
     const int chunks = (width + kChunkK - 1) / kChunkK;
     const int c0 = chunks * wave / kUpWaves, c1 = chunks * (wave + 1) / kUpWaves;
-    const bool last = blockIdx.x == gridDim.x - 1;
-    // up to 16 MT tokens from `first` on
-    auto pass = [&](auto mt, auto in_flight, int first) {
-        constexpr int N = decltype(mt)::value;
-        Row<X> tokens[N];
-        const int tiles = min(N, (mine - first + 15) / 16);
+    int set = 0;
+    for (int i = 0; i < own; ++i) {
+        const int f0 = (int(blockIdx.x) * own + i) * 16, f = min(f0 + r, hidden - 1);
+        if (f0 >= hidden) return;
+        const bool last = f0 + 16 >= hidden;
+        const Row<W> rows[2] = {gate.row(e, f), up.row(e, f)};
+        // up to 16 N tokens from `first` on
+        auto pass = [&](auto mt, auto in_flight, int first) {
+            constexpr int N = decltype(mt)::value;
+            Row<X> tokens[N];
+            const int tiles = min(N, (mine - first + 15) / 16);
 #pragma unroll
-        for (int m = 0; m < N; ++m)
-            tokens[m] = {x + int64_t(s_token[min(first + 16 * m + r, mine - 1)]) * ld_x};
-        f32x4 acc[2][N] = {};
-        accumulate<decltype(in_flight)::value>(acc, rows, tokens, c0, c1, width, g, tiles);
+            for (int m = 0; m < N; ++m)
+                tokens[m] = {x + int64_t(s_token[min(first + 16 * m + r, mine - 1)]) * ld_x};
+            f32x4 acc[2][N] = {};
+            accumulate<decltype(in_flight)::value>(acc, rows, tokens, c0, c1, width, g);
 #pragma unroll
-        for (int m = 0; m < N; ++m) {
-            if (m >= tiles) continue;
-            parts[wave][0][lane] = acc[0][m];
-            parts[wave][1][lane] = acc[1][m];
-            __syncthreads();
-            const int at = first + 16 * m + r;
-            if (wave == 0 && at < mine) {
-                f32x4 sg = parts[0][0][lane], su = parts[0][1][lane];
-#pragma unroll
-                for (int v = 1; v < kUpWaves; ++v) sg += parts[v][0][lane], su += parts[v][1][lane];
-                const int64_t base = s_slot[at] * to.padded + f0 + 4 * g;
-                bf16x4 hi, lo;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float h = f0 + 4 * g + i < hidden ? s_weight[at] * (activate<GELU>(sg[i]) * su[i]) : 0.0f;
-                    hi[i] = bf16(h);
-                    // an infinity has no second part
-                    lo[i] = __builtin_isinf(float(hi[i])) ? bf16(0.0f) : bf16(h - float(hi[i]));
-                }
-                *reinterpret_cast<bf16x4 *>(to.hi + base) = hi;
-                *reinterpret_cast<bf16x4 *>(to.lo + base) = lo;
-                if (last)  // zeros to the end of the last chunk
-                    for (int64_t f = 16; f0 + f < to.padded; f += 16) {
-                        *reinterpret_cast<bf16x4 *>(to.hi + base + f) = bf16x4{};
-                        *reinterpret_cast<bf16x4 *>(to.lo + base + f) = bf16x4{};
-                    }
+            for (int m = 0; m < N; ++m) {
+                if (m >= tiles) continue;
+                // two sets in turn: who writes one again has passed the barrier behind its reading
+                parts[set][wave][0][lane] = acc[0][m];
+                parts[set][wave][1][lane] = acc[1][m];
+                lds_barrier();
+                const int at = first + 16 * m + r;
+                if (wave == set && at < mine)
+                    store_hidden<GELU>(parts[set], lane, f0, hidden, last, s_slot[at], s_weight[at], to);
+                set ^= 1;
             }
-            __syncthreads();
+        };
+        using std::integral_constant;
+        for (int first = 0; first < mine; first += 16 * MT) {
+            if (MT > 1 && mine - first > 16) pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
+            else pass(integral_constant<int, 1>{}, integral_constant<int, (std::is_same_v<W, Mx4> ? 4 : 2)>{}, first);
         }
-    };
-    using std::integral_constant;
-    for (int first = 0; first < mine; first += 16 * MT) {
-        if (MT > 1 && mine - first > 16) pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
-        else pass(integral_constant<int, 1>{}, integral_constant<int, (std::is_same_v<W, Mx4> ? 4 : 2)>{}, first);
     }
 }
 
+// A row of staged tokens: whole chunks, and 16 bytes so that the rows' starts lie in different banks.
+__host__ __device__ constexpr int staged_row(int width) { return (width + kChunkK - 1) / kChunkK * kChunkK + 8; }
+
+// The same with few choices: no list is built, and the weights are under way after one load. STAGE: the expert's tokens
+// go to LDS first.
+template <typename W, typename X, bool GELU, bool STAGE>
+__global__ __launch_bounds__(64 * kUpWaves, STAGE ? 4 : 2) void k_experts_up_few(Choices ch, const X *__restrict__ x, int64_t ld_x,
+                                                                     Matrix<W> gate, Matrix<W> up, int width, int hidden,
+                                                                     Between to) {
+    extern __shared__ __align__(16) char smem[];  // the staged tokens
+    __shared__ f32x4 parts[kUpWaves][2][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const Few few(ch, lane);
+    if (int(blockIdx.y) >= few.count()) return;
+    const int e = few.number(blockIdx.y);
+    int token;
+    uint64_t choices;
+    const int mine = few.tokens(e, lane, token, choices);
+    const int f0 = int(blockIdx.x) * 16, f = min(f0 + r, hidden - 1);
+    const int chunks = (width + kChunkK - 1) / kChunkK;
+    const Row<W> rows[2] = {gate.row(e, f), up.row(e, f)};
+    f32x4 acc[2][1] = {};
+    const int c0 = chunks * wave / kUpWaves, c1 = chunks * (wave + 1) / kUpWaves;
+    constexpr int U = std::is_same_v<W, Mx4> ? 4 : 2;
+    if constexpr (STAGE) {
+        const int row = staged_row(width);
+        X *staged = reinterpret_cast<X *>(smem);
+        for (int t = 0; t < mine; ++t) {
+            const uint16_t *from = reinterpret_cast<const uint16_t *>(x + int64_t(__shfl(token, t)) * ld_x);
+            for (int k = 8 * int(threadIdx.x); k < chunks * kChunkK; k += 8 * 64 * kUpWaves)
+                *reinterpret_cast<i32x4 *>(staged + t * row + k) = load_half(from, k, width);
+        }
+        lds_barrier();
+        const Row<Staged<X>> tokens[1] = {{(LdsPtr<X>)(staged) + min(r, mine - 1) * row}};
+        accumulate<U>(acc, rows, tokens, c0, c1, width, g);
+    } else {
+        const Row<X> tokens[1] = {{x + int64_t(__shfl(token, min(r, mine - 1))) * ld_x}};
+        accumulate<U>(acc, rows, tokens, c0, c1, width, g);
+    }
+    parts[wave][0][lane] = acc[0][0];
+    parts[wave][1][lane] = acc[1][0];
+    __syncthreads();
+    if (wave > 0) return;
+    token = __shfl(token, r);
+    choices = uint64_t(uint32_t(__shfl(int(choices >> 32), r))) << 32 | uint32_t(__shfl(int(choices), r));
+    const int at = token * ch.top_k, slot = at + __builtin_ctzll(choices | uint64_t(1) << 63);
+    float weight = __shfl(few.weight, slot);
+    for (uint64_t more = choices & (choices - 1); __any(more != 0); more &= more - 1) {
+        const float w = __shfl(few.weight, at + __builtin_ctzll(more | uint64_t(1) << 63));
+        if (more) weight += w;
+    }
+    if (r >= mine) return;
+    store_hidden<GELU>(parts, lane, f0, hidden, f0 + 16 >= hidden, slot, weight, to);
+}
+
 // A wave takes an equal run of the contraction over (expert in use, chunk of hidden units) for 16 columns, the tokens
-// of an expert 16 MT at a time, and adds each expert's results to its own sums of every token, in LDS.
-template <typename W, typename X, int MT>
-__global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Between from, Matrix<W> down, int tokens, int hidden,
+// of an expert 16 MT at a time, and adds each expert's results to its own sums of every token, in LDS. FEW: as above.
+// STAGE: the hidden values of all slots go to LDS first.
+template <typename W, typename X, int MT, bool FEW, bool STAGE>
+__global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Between from, Matrix<W> down, int hidden,
                                                                   int width, X *__restrict__ out, int64_t ld_out) {
     extern __shared__ __align__(16) char smem[];
     f32x4 *sums = reinterpret_cast<f32x4 *>(smem);  // [wave][token][4 columns]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int n0 = int(blockIdx.x) * 16, group = blockIdx.y, t0 = group * kGroup;
-    const int count = min(kGroup, tokens - t0);
+    const int count = min(kGroup, ch.tokens - t0);
     const int n = min(n0 + r, width - 1);
     f32x4 *own = sums + wave * count * 4;
     for (int i = lane; i < count * 4; i += 64) own[i] = f32x4{};
-    const int chunks = (hidden + kChunkK - 1) / kChunkK;
-    const int64_t all = int64_t(*from.count) * chunks;
-    int64_t u = all * wave / kDownWaves;
-    const int64_t end = all * (wave + 1) / kDownWaves;
-    // an expert's number, list and first token of the list are loaded while the one before is multiplied
-    struct Next {
-        int expert, first, last;
-        int2 entry;
-    };
-    auto look = [&](int a) {
-        const int *b = from.bounds + int64_t(a) * (kGroups + 1) + group;
-        Next x{from.expert[a], b[0], b[1], make_int2(0, 0)};
-        x.entry = from.list[int64_t(a) * tokens + max(min(x.first + r, x.last - 1), 0)];
-        return x;
-    };
-    int a = int(u / chunks);
-    Next next{};
-    if (u < end) next = look(a);
-    for (; u < end; ++a) {
-        const Next now = next;
-        const int c0 = int(u - int64_t(a) * chunks), c1 = int(min(int64_t(chunks), c0 + (end - u)));
-        u += c1 - c0;
-        if (u < end) next = look(a + 1);
-        const Row<W> rows[1] = {down.row(now.expert, n)};
-        auto pass = [&](auto mt, auto in_flight, int first) {
-            constexpr int N = decltype(mt)::value;
-            Row<Planes> x[N];
-            int2 entry[N];
-            const int tiles = min(N, (now.last - first + 15) / 16);
-#pragma unroll
-            for (int m = 0; m < N; ++m) {
-                entry[m] = m == 0 && first == now.first
-                               ? now.entry
-                               : from.list[int64_t(a) * tokens + min(first + 16 * m + r, now.last - 1)];
-                const int64_t base = entry[m].y * from.padded;
-                x[m] = {from.hi + base, from.lo + base};
-            }
-            f32x4 part[1][N] = {};
-            accumulate<decltype(in_flight)::value>(part, rows, x, c0, c1, hidden, g, tiles);
-#pragma unroll
-            for (int m = 0; m < N; ++m)
-                if (first + 16 * m + r < now.last) own[(entry[m].x - t0) * 4 + g] += part[0][m];
-        };
-        using std::integral_constant;
-        for (int first = now.first; first < now.last; first += 16 * MT) {
-            if (MT > 1 && now.last - first > 16) pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
-            else pass(integral_constant<int, 1>{}, integral_constant<int, 2>{}, first);
+    using H = std::conditional_t<STAGE, Staged<Planes>, Planes>;
+    bf16 *staged = reinterpret_cast<bf16 *>(sums + kDownWaves * count * 4);
+    const int slots = ch.tokens * ch.top_k, row = staged_row(hidden), lds_lo = slots * row;
+    if constexpr (STAGE) {
+        const int per_row = int(from.padded) / 8;
+        for (int i = threadIdx.x; i < slots * per_row; i += 64 * kDownWaves) {
+            const int s = i / per_row, k = (i - s * per_row) * 8;
+            *reinterpret_cast<i32x4 *>(staged + s * row + k) =
+                *reinterpret_cast<const i32x4 *>(from.hi + s * from.padded + k);
+            *reinterpret_cast<i32x4 *>(staged + lds_lo + s * row + k) =
+                *reinterpret_cast<const i32x4 *>(from.lo + s * from.padded + k);
         }
+        lds_barrier();
+    }
+    const int chunks = (hidden + kChunkK - 1) / kChunkK;
+    // an expert's number, how many tokens it has, and of the first 16 the lane's token and slot
+    struct Work {
+        int expert, tokens, token, slot;
+    };
+    auto walk = [&](int used, auto &&look) {
+        const int64_t all = int64_t(used) * chunks, end = all * (wave + 1) / kDownWaves;
+        int64_t u = all * wave / kDownWaves;
+        int a = int(u / chunks);
+        Work next{};
+        if (u < end) next = look(a);
+        for (; u < end; ++a) {
+            const Work now = next;
+            const int c0 = int(u - int64_t(a) * chunks), c1 = int(min(int64_t(chunks), c0 + (end - u)));
+            u += c1 - c0;
+            if (u < end) next = look(a + 1);  // loaded while this one is multiplied
+            const Row<W> rows[1] = {down.row(now.expert, n)};
+            auto pass = [&](auto mt, auto in_flight, int first) {
+                constexpr int N = decltype(mt)::value;
+                Row<H> x[N];
+                int token[N];
+                bool live[N];
+#pragma unroll
+                for (int m = 0; m < N; ++m) {
+                    int2 entry = make_int2(now.token, now.slot);
+                    if constexpr (N > 1)
+                        entry = from.list[(int64_t(a) * from.groups + group) * kGroup +
+                                          min(first + 16 * m + r, now.tokens - 1)];
+                    else if (!FEW && first > 0)
+                        entry = from.list[(int64_t(a) * from.groups + group) * kGroup + min(first + r, now.tokens - 1)];
+                    token[m] = entry.x;
+                    live[m] = first + 16 * m + r < now.tokens;
+                    if constexpr (STAGE) {
+                        const LdsPtr<bf16> at = (LdsPtr<bf16>)(staged) + (live[m] ? entry.y : 0) * row;
+                        x[m] = {at, at + lds_lo};
+                    } else {
+                        const int64_t base = (live[m] ? entry.y : 0) * from.padded;
+                        x[m] = {from.hi + base, from.lo + base};
+                    }
+                }
+                f32x4 part[1][N] = {};
+                accumulate<decltype(in_flight)::value>(part, rows, x, c0, c1, hidden, g);
+#pragma unroll
+                for (int m = 0; m < N; ++m)
+                    if (live[m]) own[(token[m] - t0) * 4 + g] += part[0][m];
+            };
+            using std::integral_constant;
+            for (int first = 0; first < now.tokens; first += 16 * MT) {
+                if (MT > 1 && now.tokens - first > 16)
+                    pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
+                else pass(integral_constant<int, 1>{}, integral_constant<int, (std::is_same_v<W, f16> ? 2 : 4)>{}, first);
+            }
+        }
+    };
+    if constexpr (FEW) {
+        const Few few(ch, lane);
+        walk(few.count(), [&](int a) {
+            Work w;
+            uint64_t choices;
+            w.expert = few.number(a);
+            w.tokens = few.tokens(w.expert, lane, w.token, choices);
+            w.slot = w.token * ch.top_k + __builtin_ctzll(choices | uint64_t(1) << 63);
+            w.token = __shfl(w.token, r);
+            w.slot = __shfl(w.slot, r);
+            return w;
+        });
+    } else {
+        walk(*from.count, [&](int a) {
+            const int64_t at = int64_t(a) * from.groups + group;
+            const int2 entry = from.list[at * kGroup + r];  // past the list's end: not used
+            return Work{from.expert[a], from.counts[at], entry.x, entry.y};
+        });
     }
     __syncthreads();
     for (int i = threadIdx.x; i < count * 4; i += 64 * kDownWaves) {
@@ -298,6 +447,7 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, void *ws, Between *to) {
     const int64_t slots = tokens * top_k, most = std::min(slots, experts);
+    const int64_t padded = (hidden + kChunkK - 1) / kChunkK * kChunkK;
     char *p = static_cast<char *>(ws);
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -305,18 +455,19 @@ size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, voi
         at += up256(bytes);
         return p + a;
     };
-    const int64_t padded = (hidden + kChunkK - 1) / kChunkK * kChunkK;
-    char *count = take(4), *expert = take(size_t(most) * 4), *bounds = take(size_t(most) * (kGroups + 1) * 4);
-    char *list = take(size_t(most) * size_t(tokens) * 8);
+    const int64_t groups = (tokens + kGroup - 1) / kGroup;
+    char *count = take(4), *expert = take(size_t(most) * 4), *counts = take(size_t(most * groups) * 4);
+    char *list = take(size_t(most * groups) * kGroup * 8);
     char *hi = take(size_t(slots) * size_t(padded) * 2), *lo = take(size_t(slots) * size_t(padded) * 2);
     if (to) {
         to->count = reinterpret_cast<int *>(count);
         to->expert = reinterpret_cast<int *>(expert);
-        to->bounds = reinterpret_cast<int *>(bounds);
+        to->counts = reinterpret_cast<int *>(counts);
         to->list = reinterpret_cast<int2 *>(list);
         to->hi = reinterpret_cast<bf16 *>(hi);
         to->lo = reinterpret_cast<bf16 *>(lo);
         to->padded = padded;
+        to->groups = int(groups);
     }
     return at;
 }
@@ -339,22 +490,43 @@ template <typename W, typename X, bool GELU>
 void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matrix &gate, const vspmm_expert_matrix &up,
             const vspmm_expert_matrix &down, int width, int hidden, X *out, int64_t ld_out, const Between &b,
             hipStream_t s) {
-    const dim3 grid((hidden + 15) / 16, std::min(ch.tokens * ch.top_k, ch.experts));
-    if (ch.tokens <= 16)
-        hipLaunchKernelGGL((k_experts_up<W, X, GELU, 1>), grid, dim3(64 * kUpWaves), 0, s, ch, x, ld_x, matrix<W>(gate),
-                           matrix<W>(up), width, hidden, b);
-    else
-        hipLaunchKernelGGL((k_experts_up<W, X, GELU, 4>), grid, dim3(64 * kUpWaves), 0, s, ch, x, ld_x, matrix<W>(gate),
-                           matrix<W>(up), width, hidden, b);
-    auto go = [&](auto mt) {
+    const int tiles = (hidden + 15) / 16, most = std::min(ch.tokens * ch.top_k, ch.experts);
+    const bool few = ch.tokens <= 16 && ch.tokens * ch.top_k <= 64;
+    if (few) {
+        auto go = [&](auto stage, size_t lds) {
+            hipLaunchKernelGGL((k_experts_up_few<W, X, GELU, decltype(stage)::value>), dim3(tiles, most),
+                               dim3(64 * kUpWaves), lds, s, ch, x, ld_x, matrix<W>(gate), matrix<W>(up), width, hidden,
+                               b);
+        };
+        const size_t lds = size_t(ch.tokens) * staged_row(width) * 2;
+        if (lds <= kStageMax) go(std::true_type{}, lds);
+        else go(std::false_type{}, 0);
+    } else {
+        // a block builds its expert's list once for up to four runs of hidden units, while there are blocks for all
+        const int own = std::max(1, std::min(4, int(int64_t(tiles) * most / 1024)));
+        const dim3 grid((tiles + own - 1) / own, most);
+        auto go = [&](auto mt) {
+            hipLaunchKernelGGL((k_experts_up<W, X, GELU, decltype(mt)::value>), grid, dim3(64 * kUpWaves), 0, s, ch, x,
+                               ld_x, matrix<W>(gate), matrix<W>(up), width, hidden, own, b);
+        };
+        if (ch.tokens <= 16) go(std::integral_constant<int, 1>{});
+        else go(std::integral_constant<int, 4>{});
+    }
+    auto go = [&](auto mt, auto by_few, auto stage, size_t staged) {
         constexpr int MT = decltype(mt)::value;
-        const size_t lds = size_t(kDownWaves) * std::min(ch.tokens, kGroup) * 64;
-        allow_lds(reinterpret_cast<const void *>(&k_experts_down<W, X, MT>), lds);
-        hipLaunchKernelGGL((k_experts_down<W, X, MT>), dim3((width + 15) / 16, (ch.tokens + kGroup - 1) / kGroup),
-                           dim3(64 * kDownWaves), lds, s, b, matrix<W>(down), ch.tokens, hidden, width, out, ld_out);
+        constexpr bool FEW = decltype(by_few)::value, STAGE = decltype(stage)::value;
+        const size_t lds = size_t(kDownWaves) * std::min(ch.tokens, kGroup) * 64 + staged;
+        allow_lds(reinterpret_cast<const void *>(&k_experts_down<W, X, MT, FEW, STAGE>), lds);
+        hipLaunchKernelGGL((k_experts_down<W, X, MT, FEW, STAGE>),
+                           dim3((width + 15) / 16, (ch.tokens + kGroup - 1) / kGroup), dim3(64 * kDownWaves), lds, s, ch,
+                           b, matrix<W>(down), hidden, width, out, ld_out);
     };
-    if (ch.tokens <= 16) go(std::integral_constant<int, 1>{});
-    else go(std::integral_constant<int, 4>{});
+    constexpr std::integral_constant<int, 1> one{};
+    const size_t staged = size_t(ch.tokens) * ch.top_k * staged_row(hidden) * 4;
+    if (few && staged <= 2 * kStageMax) go(one, std::true_type{}, std::true_type{}, staged);
+    else if (few) go(one, std::true_type{}, std::false_type{}, 0);
+    else if (ch.tokens <= 16) go(one, std::false_type{}, std::false_type{}, 0);
+    else go(std::integral_constant<int, 4>{}, std::false_type{}, std::false_type{}, 0);
 }
 
 }  // namespace

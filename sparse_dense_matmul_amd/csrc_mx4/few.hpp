@@ -30,6 +30,29 @@ struct Row<Planes> {  // whole chunks: zeros past the width
 };
 
 template <typename T>
+struct Staged {};  // rows of T that lie in LDS, whole chunks with zeros at the end
+template <typename T>
+using LdsPtr = const __attribute__((address_space(3))) T *;
+template <typename T>
+struct Row<Staged<T>> {
+    LdsPtr<T> p;
+};
+template <>
+struct Row<Staged<Planes>> {
+    LdsPtr<bf16> hi, lo;
+};
+template <typename X>
+struct Plain {  // what a row's values are, wherever they lie
+    using type = X;
+    static constexpr bool staged = false;
+};
+template <typename T>
+struct Plain<Staged<T>> {
+    using type = T;
+    static constexpr bool staged = true;
+};
+
+template <typename T>
 struct Piece {  // a lane's part of a chunk
     i32x4 v[4];
 };
@@ -91,7 +114,12 @@ struct Step {
 template <bool WHOLE, typename T>
 __device__ __forceinline__ Step<T> load_step(const Row<T> &row, int k, int width) {
     Step<T> s;
-    if constexpr (std::is_same_v<T, Planes>) {
+    if constexpr (std::is_same_v<T, Staged<Planes>>) {
+        s.hi = *reinterpret_cast<LdsPtr<i32x4>>(row.hi + k);
+        s.lo = *reinterpret_cast<LdsPtr<i32x4>>(row.lo + k);
+    } else if constexpr (Plain<T>::staged) {
+        s.hi = *reinterpret_cast<LdsPtr<i32x4>>(row.p + k);
+    } else if constexpr (std::is_same_v<T, Planes>) {
         s.hi = *reinterpret_cast<const i32x4 *>(row.hi + k);
         s.lo = *reinterpret_cast<const i32x4 *>(row.lo + k);
     } else if (WHOLE) {
@@ -120,9 +148,10 @@ __device__ __forceinline__ float scale_operand_of(uint32_t scales, int j) {
 // tile: as many instructions as the two have parts.
 template <typename T, typename X>
 __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 c) {
-    if constexpr (std::is_same_v<X, T>) {
+    using V = typename Plain<X>::type;
+    if constexpr (std::is_same_v<V, T>) {
         return mma16<T>(a, x.hi, c);
-    } else if constexpr (std::is_same_v<X, Planes>) {
+    } else if constexpr (std::is_same_v<V, Planes>) {
         i32x4 hi = a, lo;
         if constexpr (std::is_same_v<T, f16>) split(a, hi, lo);
         c = mma16<bf16>(hi, x.hi, c);
@@ -141,90 +170,105 @@ __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 
 // Whether a wave's chunk of a matrix may meet its tokens in float16: each lane answers for the block it loaded.
 __device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) { return __all(f16_scale(w.scale >> (8 * g) & 255)); }
 
-// acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values, U chunks of rows in flight.
-// Tiles of tokens from `tiles` on are neither read nor multiplied. One tile's tokens are loaded with the rows, those of
-// several beside the products, which would need more registers than there are otherwise.
+// acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values, U at a time. One tile's tokens are
+// loaded by chunks; those of several, which would need more registers than there are, and those in LDS beside the
+// products.
 template <int U, typename W, typename X, int R, int MT>
 __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&rows)[R], const Row<X> (&x)[MT], int c0,
-                                           int c1, int width, int g, int tiles = MT) {
+                                           int c1, int width, int g) {
     constexpr bool BOTH = std::is_same_v<X, Mx4>, CODES = std::is_same_v<W, Mx4>;
+    constexpr bool BY_CHUNKS = BOTH || (MT == 1 && !Plain<X>::staged);
+    using V = typename Plain<X>::type;
     const int whole = min(width / kChunkK, c1);
     int c = c0;
+    // N chunks: all are on their way before the first is waited for, as far as the compiler leaves it so
+    auto load_rows = [&](auto &w, int at) {
+#pragma unroll
+        for (auto &u : w) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) load_piece<BOTH>(u[i], rows[i], at * kChunkK, g);
+            ++at;
+        }
+    };
+    auto load_tokens = [&](auto &t, int at) {
+        if constexpr (BY_CHUNKS) {
+#pragma unroll
+            for (auto &u : t) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    load_piece<BOTH>(u[m], x[m], at * kChunkK, g);
+                ++at;
+            }
+        }
+    };
+    auto multiply = [&](const Piece<W> (&w)[R], const Piece<V> (&t)[BY_CHUNKS ? MT : 1], int at) {
+        if constexpr (BOTH) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    acc[i][m] = mma16_mx4<0>(w[i].codes, w[i].scale, t[m].codes, t[m].scale, acc[i][m]);
+        } else {
+            i32x4 codes[R];
+            if constexpr (CODES) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) codes[i] = exchange(w[i].codes);
+            }
+            auto chunk = [&](auto type) {
+                using T = decltype(type);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    i32x4 a[R];
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        if constexpr (CODES) a[i] = widen<T>(uint32_t(codes[i][j]), scale_operand_of(w[i].scale, j));
+                        else a[i] = w[i].v[j];
+                    }
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        Step<X> s;
+                        if constexpr (!BY_CHUNKS) s = load_step<true>(x[m], at * kChunkK + 32 * j + 8 * g, width);
+                        else if constexpr (std::is_same_v<V, Planes>) s.hi = t[m].hi[j], s.lo = t[m].lo[j];
+                        else s.hi = t[m].v[j];
+#pragma unroll
+                        for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[i], s, acc[i][m]);
+                    }
+                }
+            };
+            if constexpr (!CODES) {
+                chunk(W{});
+            } else if constexpr (std::is_same_v<V, f16>) {
+                // float16 tokens meet the weights in float16 where it holds them exactly, which it does for all but far
+                // scales; else in two bfloat16 parts
+                bool exact = true;
+#pragma unroll
+                for (int i = 0; i < R; ++i) exact = exact && f16_holds(w[i], g);
+                if (exact) chunk(f16{});
+                else chunk(bf16{});
+            } else {
+                chunk(bf16{});
+            }
+        }
+    };
     auto some = [&](auto count) {
         constexpr int N = decltype(count)::value;
         Piece<W> w[N][R];
-        Piece<X> t[N][MT];
+        Piece<V> t[N][BY_CHUNKS ? MT : 1];
+        load_rows(w, c);
+        load_tokens(t, c);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-#pragma unroll
-            for (int i = 0; i < R; ++i) load_piece<BOTH>(w[u][i], rows[i], (c + u) * kChunkK, g);
-            if constexpr (BOTH || MT == 1) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    if (m < tiles) load_piece<BOTH>(t[u][m], x[m], (c + u) * kChunkK, g);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            if constexpr (BOTH) {
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        if (m < tiles)
-                            acc[i][m] = mma16_mx4<0>(w[u][i].codes, w[u][i].scale, t[u][m].codes, t[u][m].scale,
-                                                     acc[i][m]);
-            } else {
-                i32x4 codes[R];
-                if constexpr (CODES) {
-#pragma unroll
-                    for (int i = 0; i < R; ++i) codes[i] = exchange(w[u][i].codes);
-                }
-                auto chunk = [&](auto type) {
-                    using T = decltype(type);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        i32x4 a[R];
-#pragma unroll
-                        for (int i = 0; i < R; ++i) {
-                            if constexpr (CODES)
-                                a[i] = widen<T>(uint32_t(codes[i][j]), scale_operand_of(w[u][i].scale, j));
-                            else a[i] = w[u][i].v[j];
-                        }
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            if (m >= tiles) continue;
-                            Step<X> s;
-                            if constexpr (MT > 1)
-                                s = load_step<true>(x[m], (c + u) * kChunkK + 32 * j + 8 * g, width);
-                            else if constexpr (std::is_same_v<X, Planes>) s.hi = t[u][m].hi[j], s.lo = t[u][m].lo[j];
-                            else s.hi = t[u][m].v[j];
-#pragma unroll
-                            for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[i], s, acc[i][m]);
-                        }
-                    }
-                };
-                if constexpr (!CODES) {
-                    chunk(W{});
-                } else if constexpr (std::is_same_v<X, f16>) {
-                    // float16 tokens meet the weights in float16 where it holds them exactly, which it does for all
-                    // but far scales; else in two bfloat16 parts
-                    bool exact = true;
-#pragma unroll
-                    for (int i = 0; i < R; ++i) exact = exact && f16_holds(w[u][i], g);
-                    if (exact) chunk(f16{});
-                    else chunk(bf16{});
-                } else {
-                    chunk(bf16{});
-                }
-            }
-        }
+        for (int u = 0; u < N; ++u) multiply(w[u], t[u], c + u);
         c += N;
     };
     while (c + U <= whole) some(std::integral_constant<int, U>{});
+    if constexpr (U > 2)
+        if (c + 2 <= whole) some(std::integral_constant<int, 2>{});
     if constexpr (U > 1)
-        while (c < whole) some(std::integral_constant<int, 1>{});
-    if (c >= c1) return;
+        if (c < whole) some(std::integral_constant<int, 1>{});
+    if (c >= c1) {
+        settle(acc);
+        return;
+    }
     // the last chunk, in parts: what lies past the width is zeros on both sides
     if constexpr (BOTH) {
         const int b = c * (kChunkK / kBlock) + g;
@@ -242,44 +286,76 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
         for (int i = 0; i < R; ++i) w[i] = part(rows[i]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            if (m >= tiles) continue;
             const Piece<Mx4> t = part(x[m]);
 #pragma unroll
             for (int i = 0; i < R; ++i) acc[i][m] = mma16_mx4<0>(w[i].codes, w[i].scale, t.codes, t.scale, acc[i][m]);
         }
     } else {
+        // blocks of 32 one after another, or, where registers allow, all loaded first; those past the end are zeros
+        constexpr int N = MT == 1 ? kChunkK / kBlock : 1;
 #pragma unroll 1
-        for (int k = c * kChunkK; k < width; k += kBlock) {
-            i32x4 a[R];
-            uint32_t word[R], top[R];
+        for (int k0 = c * kChunkK; k0 < width; k0 += N * kBlock) {
+            i32x4 a[N][R];
+            uint32_t word[N][R], top[N][R];
+            Step<X> s[N][MT];
             bool exact = true;
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
+            for (int n = 0; n < N; ++n) {
+                const int k = k0 + n * kBlock;
+                const bool here = k < width;
+                const int at = here ? k : k0;  // a block that is there: its values are not used
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    if constexpr (CODES) {
+                        const uint8_t *p = rows[i].codes + int64_t(at / kBlock) * kBlockBytes + 4 * g;
+                        word[n][i] = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(p);
+                        top[n][i] = rows[i].scales[at / kBlock];
+                    } else {
+                        a[n][i] = load_half(reinterpret_cast<const uint16_t *>(rows[i].p), k + 8 * g, width);
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    s[n][m] = load_step<false>(x[m], (Plain<X>::staged || std::is_same_v<V, Planes> ? at : k) + 8 * g,
+                                               width);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const bool here = k0 + n * kBlock < width;
                 if constexpr (CODES) {
-                    const uint8_t *p = rows[i].codes + int64_t(k / kBlock) * kBlockBytes + 4 * g;
-                    word[i] = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(p);
-                    top[i] = rows[i].scales[k / kBlock];
-                    exact = exact && f16_scale(top[i]);
-                } else {
-                    a[i] = load_half(reinterpret_cast<const uint16_t *>(rows[i].p), k + 8 * g, width);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) {
+                        word[n][i] = here ? word[n][i] : 0;
+                        top[n][i] = here ? top[n][i] : 127;
+                        if constexpr (std::is_same_v<V, f16>) exact = exact && f16_scale(top[n][i]);
+                    }
+                }
+                if constexpr (Plain<X>::staged || std::is_same_v<V, Planes>) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[n][m].hi[e] = here ? s[n][m].hi[e] : 0;
+                            if constexpr (std::is_same_v<V, Planes>) s[n][m].lo[e] = here ? s[n][m].lo[e] : 0;
+                        }
                 }
             }
             auto part = [&](auto type) {
                 using T = decltype(type);
 #pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if constexpr (CODES) a[i] = widen<T>(word[i], scale_operand(top[i]));
+                for (int n = 0; n < N; ++n) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (m >= tiles) continue;
-                    const Step<X> s = load_step<false>(x[m], k + 8 * g, width);
+                    for (int i = 0; i < R; ++i)
+                        if constexpr (CODES) a[n][i] = widen<T>(word[n][i], scale_operand(top[n][i]));
 #pragma unroll
-                    for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[i], s, acc[i][m]);
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[n][i], s[n][m], acc[i][m]);
                 }
             };
             if constexpr (!CODES) {
                 part(W{});
-            } else if constexpr (std::is_same_v<X, f16>) {
+            } else if constexpr (std::is_same_v<V, f16>) {
                 if (__all(exact)) part(f16{});
                 else part(bf16{});
             } else {
@@ -287,6 +363,7 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
             }
         }
     }
+    settle(acc);
 }
 
 }  // namespace vspmm

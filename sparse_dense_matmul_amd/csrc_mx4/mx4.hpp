@@ -118,6 +118,30 @@ __device__ __forceinline__ f32x16 mma32_mx4(i32x4 a, uint32_t sa, i32x4 b, uint3
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, I, int(sa), I, int(sb));
 }
 
+// Waits until the matrix instructions have written their sums. The compiler puts waits between such an instruction and
+// a use of its result, but here it was seen to leave them out: where a branch leads past a short block straight from
+// the instruction to the use, the first registers of the sum were read too early. So the products have no branches
+// between them that depend on data, and a sum goes through here before any use but another product.
+template <typename V, int A, int B>
+__device__ __forceinline__ void settle(V (&acc)[A][B]) {
+#pragma unroll
+    for (int i = 0; i < A; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j) asm volatile("" : "+v"(acc[i][j]));
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < A; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
+
+// A barrier for what lies in LDS: loads to registers stay on their way (__syncthreads waits for them).
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 __host__ __device__ constexpr int64_t blocks_of_width(int64_t width) { return (width + kBlock - 1) / kBlock; }
 
 }  // namespace vspmm

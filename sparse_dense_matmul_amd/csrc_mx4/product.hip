@@ -43,7 +43,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_few(Row<X> x, int64_t ld_x, 
     }
     const int chunks = (k + kChunkK - 1) / kChunkK;
     f32x4 acc[R][MT] = {};
-    accumulate<(MT == 1 ? 4 : MT == 2 ? 2 : 1)>(acc, rows, tokens, chunks * wave / kFewWaves,
+    accumulate<(MT == 1 ? 4 : 2)>(acc, rows, tokens, chunks * wave / kFewWaves,
                                                 chunks * (wave + 1) / kFewWaves, k, g);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {

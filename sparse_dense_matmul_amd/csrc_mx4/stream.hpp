@@ -191,6 +191,9 @@ __global__ __launch_bounds__(256, 1) void k_stream_both(const uint8_t *__restric
         pin(acc);
         __builtin_amdgcn_sched_barrier(0);
     }
+    pin(acc);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");  // as settle() does
+    pin(acc);
     __syncthreads();  // no copy is on its way when the block ends
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
 }
@@ -264,18 +267,15 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
         };
         auto multiply = [&](int set) {
 #pragma unroll
-            for (int j = 0; j < TW; ++j)
+            for (int j = 0; j < TW; ++j) {
+                i32x4 hi = q[set][j], lo;
+                if constexpr (!std::is_same_v<T, X>) split(q[set][j], hi, lo);
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
-                    if constexpr (std::is_same_v<T, X>) {
-                        acc[i][j] = mma32<T>(p[set][i], q[set][j], acc[i][j]);
-                    } else {
-                        i32x4 hi, lo;
-                        split(q[set][j], hi, lo);
-                        acc[i][j] = mma32<T>(p[set][i], hi, acc[i][j]);
-                        acc[i][j] = mma32<T>(p[set][i], lo, acc[i][j]);
-                    }
+                    acc[i][j] = mma32<T>(p[set][i], hi, acc[i][j]);
+                    if constexpr (!std::is_same_v<T, X>) acc[i][j] = mma32<T>(p[set][i], lo, acc[i][j]);
                 }
+            }
         };
         read(0, 0, 0);
         read_w(0, 0);
@@ -343,6 +343,9 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
         __syncthreads();
         run(bf16{});
     }
+    pin(acc);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");  // as settle() does
+    pin(acc);
     __syncthreads();  // no copy is on its way when the block ends
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
 }
@@ -488,6 +491,9 @@ __global__ __launch_bounds__(256, 1) void k_stream_grad(const X *__restrict__ dy
     } else {
         run(bf16{});
     }
+    pin(acc);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");  // as settle() does
+    pin(acc);
     __syncthreads();  // no copy is on its way when the block ends
     store_tile<TW>(acc, out, ld_out, m0 + wm, c0 + wn, s.m, s.n, lane);
 }

@@ -32,13 +32,6 @@ struct TileShape {
 __device__ __forceinline__ int group_thread() { return int(threadIdx.x) & (kTileThreads - 1); }
 __device__ __forceinline__ int group_number() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kTileThreads); }
 
-// A barrier for what lies in LDS: loads to registers stay on their way (__syncthreads waits for them).
-__device__ __forceinline__ void lds_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // Steps [first, first + steps) of a group: load(step) to registers, store(buffer) from there to LDS, compute(buffer). A
 // step is loaded before the barrier that opens the one before it.
 template <typename Load, typename Store, typename Compute>
@@ -296,22 +289,19 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile(const X *__restrict__
 
     f32x16 acc[TW][TW] = {};
     const int wm = (wave & 1) * 32 * TW, wn = (wave >> 1) * 32 * TW;
-    auto compute = [&](int buf) {
-        const i32x4 *bx = lds_x + buf * EDGE * 8, *bw = lds_w + buf * SLOTS;
-        i32x4 c[TW];
-        float sc[TW];
-        bool exact16 = true;
+    // each group has as many steps as the first: those past the end are zeros
+    const int all = (s.k + kStepHalf - 1) / kStepHalf, steps = (all + KS - 1) / KS, first = group_number() * steps;
+    auto run = [&](auto type) {
+        using T = decltype(type);
+        run_steps(first, steps, load, store, [&](int buf) {
+            const i32x4 *bx = lds_x + buf * EDGE * 8, *bw = lds_w + buf * SLOTS;
+            i32x4 c[TW];
+            float sc[TW];
 #pragma unroll
-        for (int i = 0; i < TW; ++i) {
-            c[i] = bw[(wn / 32 + i) * 64 + lane];
-            const uint32_t b = reinterpret_cast<const uint8_t *>(lds_s + buf * EDGE + wn + 32 * i + r)[g];
-            sc[i] = scale_operand(b);
-            if constexpr (std::is_same_v<X, f16>) {
-                exact16 = exact16 && f16_scale(b);
+            for (int i = 0; i < TW; ++i) {
+                c[i] = bw[(wn / 32 + i) * 64 + lane];
+                sc[i] = scale_operand(reinterpret_cast<const uint8_t *>(lds_s + buf * EDGE + wn + 32 * i + r)[g]);
             }
-        }
-        auto step = [&](auto type, auto halves) {
-            using T = decltype(type);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 i32x4 p[TW], q[TW];
@@ -319,20 +309,24 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile(const X *__restrict__
                 for (int t = 0; t < TW; ++t) q[t] = bx[place(wm + 32 * t + r, 4 * g + j)];
 #pragma unroll
                 for (int i = 0; i < TW; ++i) p[i] = widen<T>(uint32_t(c[i][j]), sc[i]);
-                multiply_tiles<T, decltype(halves)::value, TW>(acc, p, q);
+                multiply_tiles<T, !std::is_same_v<T, X>, TW>(acc, p, q);
             }
-        };
-        if constexpr (std::is_same_v<X, bf16>) {
-            step(bf16{}, std::false_type{});
-        } else {
-            if (__all(exact16)) step(f16{}, std::false_type{});
-            else step(bf16{}, std::true_type{});
-        }
+        });
     };
-
-    // each group has as many steps as the first: those past the end are zeros
-    const int all = (s.k + kStepHalf - 1) / kStepHalf, steps = (all + KS - 1) / KS, first = group_number() * steps;
-    run_steps(first, steps, load, store, compute);
+    if constexpr (std::is_same_v<X, f16>) {
+        // float16 tokens meet the rows in float16 where it holds the tile's, else in two bfloat16 parts in bfloat16: the
+        // block's threads share the rows' scales
+        bool fine = true;
+        const int rows = min(EDGE, s.n - n0);
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < int64_t(rows) * blocks; i += kTileThreads * KS)
+            fine = fine && f16_scale(scales[(n0 + i / blocks) * ld_scales + i % blocks]);
+        if (__syncthreads_and(fine)) run(f16{});
+        else run(bf16{});
+    } else {
+        run(bf16{});
+    }
+    settle(acc);
     join_groups<KS>(acc, smem);
     if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
@@ -448,6 +442,7 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile_grad(const X *__restr
     } else {
         run(bf16{});
     }
+    settle(acc);
     join_groups<KS>(acc, smem);
     if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, c0 + wn, s.m, s.n, lane);
@@ -524,6 +519,7 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile_both(const uint8_t *_
     // each group has as many steps as the first: those past the end are zeros
     const int all = (s.k + kStepCodes - 1) / kStepCodes, steps = (all + KS - 1) / KS, first = group_number() * steps;
     run_steps(first, steps, load, store, compute);
+    settle(acc);
     join_groups<KS>(acc, smem);
     if (group_number() > 0) return;
     store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
