@@ -516,7 +516,7 @@ void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matr
         constexpr int MT = decltype(mt)::value;
         constexpr bool FEW = decltype(by_few)::value, STAGE = decltype(stage)::value;
         const size_t lds = size_t(kDownWaves) * std::min(ch.tokens, kGroup) * 64 + staged;
-        allow_lds(reinterpret_cast<const void *>(&k_experts_down<W, X, MT, FEW, STAGE>), lds);
+        allow_lds<&k_experts_down<W, X, MT, FEW, STAGE>>(size_t(kDownWaves) * 16 * 64 + (STAGE ? 2 * kStageMax : 0));
         hipLaunchKernelGGL((k_experts_down<W, X, MT, FEW, STAGE>),
                            dim3((width + 15) / 16, (ch.tokens + kGroup - 1) / kGroup), dim3(64 * kDownWaves), lds, s, ch,
                            b, matrix<W>(down), hidden, width, out, ld_out);

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "vspmm.h"
 
 #include "mx4.hpp"
@@ -25,9 +27,18 @@ auto with_dense(int elt, F &&f) {
     return elt == VSPMM_ELT_BF16 ? f(bf16{}) : f(f16{});
 }
 
-// A kernel that uses more LDS than the default limit of 64 KB says so once a launch.
-[[maybe_unused]] void allow_lds(const void *fn, size_t bytes) {
-    if (bytes > 64 * 1024) (void)hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+// A kernel that may use more LDS than the default limit of 64 KB, up to `most` bytes, says so once for each device
+// (a call on the host of 1.7 us, where a launch takes 3).
+template <auto Kernel>
+void allow_lds(size_t most) {
+    static std::atomic<uint64_t> done{0};
+    int device = 0;
+    if (most <= 64 * 1024 || hipGetDevice(&device) != hipSuccess) return;
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return;
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            int(most)) == hipSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
 }
 
 vspmm_status check_dense(int64_t n, int64_t width, int64_t ld, const void *p) {

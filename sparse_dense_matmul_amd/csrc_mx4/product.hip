@@ -219,7 +219,7 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
         if (m >= 256 && n >= 256 && width % kChunkK == 0 && fill(m, n) && streams(x, ld_x) && streams(*w)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 256, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_stream<T>), kStreamLds);
+            allow_lds<&k_stream<T>>(kStreamLds);
             hipLaunchKernelGGL((k_stream<T>), dim3(tiles), dim3(256), kStreamLds, stream, static_cast<const T *>(x), ld_x,
                                w->codes, w->ld_codes, w->scales, w->ld_scales, o, ld_out, s);
             return launched();
@@ -228,7 +228,7 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
             constexpr int TW = decltype(tw)::value, KS = decltype(ks)::value;
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 64 * TW, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_tile<TW, KS, T, T>), KS * tile_lds<TW>());
+            allow_lds<&k_tile<TW, KS, T, T>>(KS * tile_lds<TW>());
             hipLaunchKernelGGL((k_tile<TW, KS, T, T>), dim3(tiles), dim3(kTileThreads * KS), KS * tile_lds<TW>(), stream,
                                static_cast<const T *>(x), ld_x, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_out, s);
@@ -252,7 +252,7 @@ vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t 
         if (m >= 256 && n % kStepHalf == 0 && fill(m, width) && streams(dout, ld_dout)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, width, n, 256, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_stream_grad<T>), kStreamGradLds);
+            allow_lds<&k_stream_grad<T>>(kStreamGradLds);
             hipLaunchKernelGGL((k_stream_grad<T>), dim3(tiles), dim3(256), kStreamGradLds, stream,
                                static_cast<const T *>(dout), ld_dout, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_grad, s);
@@ -262,7 +262,7 @@ vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t 
             constexpr int TW = decltype(tw)::value, KS = decltype(ks)::value;
             unsigned tiles;
             const TileShape s = tile_shape(m, width, n, 64 * TW, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_tile_grad<TW, KS, T>), KS * grad_lds<TW>());
+            allow_lds<&k_tile_grad<TW, KS, T>>(KS * grad_lds<TW>());
             hipLaunchKernelGGL((k_tile_grad<TW, KS, T>), dim3(tiles), dim3(kTileThreads * KS), KS * grad_lds<TW>(), stream,
                                static_cast<const T *>(dout), ld_dout, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_grad, s);
@@ -291,7 +291,7 @@ vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t w
         if (m >= 256 && n >= 256 && width % kStepCodes == 0 && fill(m, n) && streams(*x) && streams(*w)) {
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 256, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_stream_both<T>), kStreamBothLds);
+            allow_lds<&k_stream_both<T>>(kStreamBothLds);
             hipLaunchKernelGGL((k_stream_both<T>), dim3(tiles), dim3(256), kStreamBothLds, stream, x->codes,
                                x->ld_codes, x->scales, x->ld_scales, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_out, s);
@@ -301,7 +301,7 @@ vspmm_status vspmm_mx4_matmul_mx4(vspmm_elt elt, int64_t m, int64_t n, int64_t w
             constexpr int TW = decltype(tw)::value, KS = decltype(ks)::value;
             unsigned tiles;
             const TileShape s = tile_shape(m, n, width, 64 * TW, tiles);
-            allow_lds(reinterpret_cast<const void *>(&k_tile_both<TW, KS, T>), KS * both_lds<TW>());
+            allow_lds<&k_tile_both<TW, KS, T>>(KS * both_lds<TW>());
             hipLaunchKernelGGL((k_tile_both<TW, KS, T>), dim3(tiles), dim3(kTileThreads * KS), KS * both_lds<TW>(), stream, x->codes,
                                x->ld_codes, x->scales, x->ld_scales, w->codes, w->ld_codes, w->scales, w->ld_scales, o,
                                ld_out, s);

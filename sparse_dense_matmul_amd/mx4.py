@@ -66,35 +66,48 @@ def _dense(t, name, types, shape=None, dtype=None, device=None, write=False):
     return _rows(t, name, shape, dtype, device, write)
 
 
-def _bytes(t, name, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
-        raise TypeError(f"{name} must be a uint8 tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    # rows may be strided, the bytes of one are contiguous
-    return t if t.stride(-1) == 1 or t.shape[-1] <= 1 else t.contiguous()
-
-
-def _mx4(a, name, dims, device=None):
-    """An Mx4's checked arrays: (codes, scales, rows, width)."""
-    if not isinstance(a, Mx4):
-        raise TypeError(f"{name} must be an Mx4")
+def _refuse(a, name, dims, device):
+    """Raises for the first thing that is wrong with an Mx4."""
     codes, scales, width = a
-    if not isinstance(codes, torch.Tensor):
-        raise TypeError(f"{name}.codes must be a uint8 tensor")
+    for t, part in ((codes, "codes"), (scales, "scales")):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+            raise TypeError(f"{name}.{part} must be a uint8 tensor")
     if codes.dim() != dims:
         raise ValueError(f"{name}.codes has shape {tuple(codes.shape)}, expected {dims} dimensions")
     if width < 0:
         raise ValueError(f"{name}.width is negative")
     blocks = (width + BLOCK - 1) // BLOCK
-    lead = codes.shape[:-1]
-    codes = _bytes(codes, f"{name}.codes", (*lead, 16 * blocks), device)
-    scales = _bytes(scales, f"{name}.scales", (*lead, blocks), codes.device)
-    return codes, scales, lead[-1], width
+    for t, part, row, on in ((codes, "codes", 16 * blocks, device),
+                             (scales, "scales", blocks, codes.device)):
+        if not t.is_cuda:
+            raise ValueError(f"{name}.{part} must be a CUDA tensor")
+        if on is not None and t.device != on:
+            raise ValueError(f"{name}.{part} is on {t.device}, expected {on}")
+        shape = (*codes.shape[:-1], row)
+        if t.shape != shape:
+            raise ValueError(f"{name}.{part} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _mx4(a, name, dims, device=None):
+    """An Mx4's checked arrays: (codes, scales, rows, width). One condition, since
+    a call for one token takes less time on the device than on the host."""
+    if not isinstance(a, Mx4):
+        raise TypeError(f"{name} must be an Mx4")
+    codes, scales, width = a
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)):
+        _refuse(a, name, dims, device)
+    shape, blocks = codes.shape, (width + BLOCK - 1) // BLOCK
+    if (len(shape) != dims or shape[-1] != 16 * blocks or scales.shape != (*shape[:-1], blocks)
+            or codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or width < 0
+            or not codes.is_cuda or scales.device != (device or codes.device)
+            or (device is not None and codes.device != device)):
+        _refuse(a, name, dims, device)
+    # rows may be strided, the bytes of one are contiguous
+    if codes.stride(-1) != 1 and shape[-1] > 1:
+        codes = codes.contiguous()
+    if scales.stride(-1) != 1 and blocks > 1:
+        scales = scales.contiguous()
+    return codes, scales, shape[-2], width
 
 
 def _struct(codes, scales):
