@@ -22,8 +22,10 @@ namespace {
 
 constexpr int kTokensMax = 1024;
 constexpr int kExpertsMax = 4096;
-constexpr int kUpWaves = 8;     // of a block of the first launch
-constexpr int kDownWaves = 8;  // of a block of the second
+constexpr int kLogWaves = 3;
+constexpr int kUpWaves = 1 << kLogWaves;  // of a block of the first launch
+constexpr int kDownWaves = 8;             // of a block of the second
+constexpr int kSplitsMax = 8;
 constexpr size_t kStageMax = 48 * 1024;  // bytes of staged tokens that leave room for two blocks
 
 // ------------------------------------------------------------------ kernels
@@ -51,6 +53,15 @@ struct Between {
     bf16 *hi, *lo;        // [slots, padded]
     int64_t padded;
     int groups;
+    // of a result whose experts are split over blocks: the parts, [splits, tokens, tiles, 16], and how many have come
+    float *parts;
+    int *arrived;  // [groups, tiles], zeroed by the first launch
+    int tiles, splits;
+
+    __device__ __forceinline__ void reset() const {
+        if (splits > 1 && blockIdx.x == 0 && blockIdx.y == 0)
+            for (int i = threadIdx.x; i < groups * tiles; i += blockDim.x) arrived[i] = 0;
+    }
 };
 
 // Up to 64 choices of up to 16 tokens: a wave holds them all, one a lane, and finds the experts in use, in order of
@@ -111,12 +122,17 @@ __device__ __forceinline__ float activate(float g) {
 
 // The hidden values of 16 units of the weights' rows f0 .. for a tile of 16 tokens from the waves' parts, by one wave:
 // lane (r, g) has token r's units f0 + 4 g .. + 3.
-template <bool GELU, int WAVES>
-__device__ __forceinline__ void store_hidden(const f32x4 (&parts)[WAVES][2][64], int lane, int f0, int hidden, bool last,
+template <bool GELU>
+__device__ __forceinline__ void store_hidden(const f32x4 (*parts)[2][64], int waves, int lane, int f0, int hidden,
                                              int slot, float weight, const Between &to) {
-    f32x4 sg = parts[0][0][lane], su = parts[0][1][lane];
+    f32x4 sg{}, su{};
 #pragma unroll
-    for (int v = 1; v < WAVES; ++v) sg += parts[v][0][lane], su += parts[v][1][lane];
+    for (int v = 0; v < kUpWaves; ++v) {  // all loaded at once: those of other runs count as zeros
+        const int from = min(v, waves - 1);
+        const f32x4 a = parts[from][0][lane], b = parts[from][1][lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sg[i] += v < waves ? a[i] : 0.0f, su[i] += v < waves ? b[i] : 0.0f;
+    }
     const int f = f0 + 4 * (lane >> 4);
     const int64_t base = slot * to.padded + f;
     bf16x4 hi, lo;
@@ -129,26 +145,36 @@ __device__ __forceinline__ void store_hidden(const f32x4 (&parts)[WAVES][2][64],
     }
     *reinterpret_cast<bf16x4 *>(to.hi + base) = hi;
     *reinterpret_cast<bf16x4 *>(to.lo + base) = lo;
-    if (last)  // zeros to the end of the last chunk
+    if (f0 + 16 >= hidden)  // zeros to the end of the last chunk
         for (int64_t i = 16; f + i < to.padded; i += 16) {
             *reinterpret_cast<bf16x4 *>(to.hi + base + i) = bf16x4{};
             *reinterpret_cast<bf16x4 *>(to.lo + base + i) = bf16x4{};
         }
 }
 
-// A block takes `own` runs of 16 hidden units of one expert, its waves an eighth of the contraction each.
-template <typename W, typename X, bool GELU, int MT>
-__global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const X *__restrict__ x, int64_t ld_x,
+// 4-bit rows and float16 tokens, multiplied in either type, need more than the 128 registers that let two blocks share a
+// compute unit (which takes the first launch of 13 tokens through 39 experts of 1,008 x 736 from 50 to 40 us).
+template <typename W, typename X>
+constexpr bool kWide = std::is_same_v<W, Mx4> && std::is_same_v<X, f16>;
+
+// `share` of a block's waves take 16 hidden units of one expert, an equal part of the contraction each, so that the
+// block has kUpWaves / share runs of units at once; it does so `own` times. ALL: `share` is all of them, which as a
+// constant takes 64 tokens to 8 of 128 experts of 4,096 x 1,024 from 460 to 415 us. Fewer share narrow tokens, so that
+// each wave has two chunks or more (13 tokens to 4 of 60 experts of 256 x 2,048: 24 us, 112 with all).
+template <typename W, typename X, bool GELU, int MT, bool ALL>
+__global__ __launch_bounds__(64 * kUpWaves, (MT == 1 && !kWide<W, X> ? 4 : 1)) void k_experts_up(Choices ch, const X *__restrict__ x, int64_t ld_x,
                                                               Matrix<W> gate, Matrix<W> up, int width, int hidden,
-                                                              int own, Between to) {
+                                                              int log_share, int own, Between to) {
     __shared__ uint32_t used[kExpertsMax / 32];
-    __shared__ int s_expert, s_total, s_counts[kTokensMax / 64];
-    __shared__ int s_slot[kTokensMax];
-    __shared__ float s_weight[kTokensMax];
-    __shared__ uint16_t s_token[kTokensMax];
+    constexpr int RUNS = MT == 1 ? 1 : kTokensMax / 64 / kUpWaves;  // one tile: no more than 16 tokens
+    __shared__ int s_expert, s_total, s_counts[RUNS * kUpWaves];
+    __shared__ int s_slot[RUNS * kUpWaves * 64];
+    __shared__ float s_weight[RUNS * kUpWaves * 64];
+    __shared__ uint16_t s_token[RUNS * kUpWaves * 64];
     __shared__ f32x4 parts[2][kUpWaves][2][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slots = ch.tokens * ch.top_k, a = blockIdx.y;
+    to.reset();
 
     // the experts in use as bits, and the a-th of them
     const int words = (ch.experts + 31) / 32;
@@ -184,7 +210,6 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
     const int e = s_expert;
 
     // its tokens in order, each with its first slot here and the sum of its weights
-    constexpr int RUNS = kTokensMax / 64 / kUpWaves;
     int slot[RUNS];
     float weight[RUNS];
     uint64_t here[RUNS];
@@ -225,17 +250,20 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
                     make_int2(run * 64 + lane, slot[i]);
         }
     }
-    for (int c = 0; c < kTokensMax / 64; ++c) mine += s_counts[c];
+    for (int c = 0; c < RUNS * kUpWaves; ++c) mine += s_counts[c];
     __syncthreads();
 
     const int r = lane & 15, g = lane >> 4;
     const int chunks = (width + kChunkK - 1) / kChunkK;
-    const int c0 = chunks * wave / kUpWaves, c1 = chunks * (wave + 1) / kUpWaves;
+    if constexpr (ALL) log_share = kLogWaves;
+    const int share = 1 << log_share, sub = wave & (share - 1), lead = wave - sub;
+    const int at_once = 16 * kUpWaves >> log_share;
+    const int c0 = chunks * sub >> log_share, c1 = chunks * (sub + 1) >> log_share;
     int set = 0;
     for (int i = 0; i < own; ++i) {
-        const int f0 = (int(blockIdx.x) * own + i) * 16, f = min(f0 + r, hidden - 1);
-        if (f0 >= hidden) return;
-        const bool last = f0 + 16 >= hidden;
+        const int64_t start = (int64_t(blockIdx.x) * own + i) * at_once;
+        if (start >= hidden) return;
+        const int f0 = int(start) + 16 * (wave >> log_share), f = min(f0 + r, hidden - 1);
         const Row<W> rows[2] = {gate.row(e, f), up.row(e, f)};
         // up to 16 N tokens from `first` on
         auto pass = [&](auto mt, auto in_flight, int first) {
@@ -255,8 +283,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void k_experts_up(Choices ch, const 
                 parts[set][wave][1][lane] = acc[1][m];
                 lds_barrier();
                 const int at = first + 16 * m + r;
-                if (wave == set && at < mine)
-                    store_hidden<GELU>(parts[set], lane, f0, hidden, last, s_slot[at], s_weight[at], to);
+                if (sub == (set & (share - 1)) && at < mine && f0 < hidden)
+                    store_hidden<GELU>(&parts[set][lead], share, lane, f0, hidden, s_slot[at], s_weight[at], to);
                 set ^= 1;
             }
         };
@@ -273,25 +301,29 @@ __host__ __device__ constexpr int staged_row(int width) { return (width + kChunk
 
 // The same with few choices: no list is built, and the weights are under way after one load. STAGE: the expert's tokens
 // go to LDS first.
-template <typename W, typename X, bool GELU, bool STAGE>
-__global__ __launch_bounds__(64 * kUpWaves, STAGE ? 4 : 2) void k_experts_up_few(Choices ch, const X *__restrict__ x, int64_t ld_x,
+template <typename W, typename X, bool GELU, bool STAGE, bool ALL>
+__global__ __launch_bounds__(64 * kUpWaves, (STAGE || !kWide<W, X> ? 4 : 1)) void k_experts_up_few(Choices ch, const X *__restrict__ x, int64_t ld_x,
                                                                      Matrix<W> gate, Matrix<W> up, int width, int hidden,
-                                                                     Between to) {
+                                                                     int log_share, Between to) {
     extern __shared__ __align__(16) char smem[];  // the staged tokens
     __shared__ f32x4 parts[kUpWaves][2][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
+    to.reset();
     const Few few(ch, lane);
     if (int(blockIdx.y) >= few.count()) return;
     const int e = few.number(blockIdx.y);
     int token;
     uint64_t choices;
     const int mine = few.tokens(e, lane, token, choices);
-    const int f0 = int(blockIdx.x) * 16, f = min(f0 + r, hidden - 1);
+    if constexpr (ALL) log_share = kLogWaves;
+    const int share = 1 << log_share, sub = wave & (share - 1);
+    const int f0 = 16 * (int(blockIdx.x) * (kUpWaves >> log_share) + (wave >> log_share));
+    const int f = min(f0 + r, hidden - 1);
     const int chunks = (width + kChunkK - 1) / kChunkK;
     const Row<W> rows[2] = {gate.row(e, f), up.row(e, f)};
     f32x4 acc[2][1] = {};
-    const int c0 = chunks * wave / kUpWaves, c1 = chunks * (wave + 1) / kUpWaves;
+    const int c0 = chunks * sub >> log_share, c1 = chunks * (sub + 1) >> log_share;
     constexpr int U = std::is_same_v<W, Mx4> ? 4 : 2;
     if constexpr (STAGE) {
         const int row = staged_row(width);
@@ -311,7 +343,7 @@ __global__ __launch_bounds__(64 * kUpWaves, STAGE ? 4 : 2) void k_experts_up_few
     parts[wave][0][lane] = acc[0][0];
     parts[wave][1][lane] = acc[1][0];
     __syncthreads();
-    if (wave > 0) return;
+    if (sub > 0 || f0 >= hidden) return;
     token = __shfl(token, r);
     choices = uint64_t(uint32_t(__shfl(int(choices >> 32), r))) << 32 | uint32_t(__shfl(int(choices), r));
     const int at = token * ch.top_k, slot = at + __builtin_ctzll(choices | uint64_t(1) << 63);
@@ -321,7 +353,7 @@ __global__ __launch_bounds__(64 * kUpWaves, STAGE ? 4 : 2) void k_experts_up_few
         if (more) weight += w;
     }
     if (r >= mine) return;
-    store_hidden<GELU>(parts, lane, f0, hidden, f0 + 16 >= hidden, slot, weight, to);
+    store_hidden<GELU>(&parts[wave], share, lane, f0, hidden, slot, weight, to);
 }
 
 // A wave takes an equal run of the contraction over (expert in use, chunk of hidden units) for 16 columns, the tokens
@@ -359,8 +391,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
         int expert, tokens, token, slot;
     };
     auto walk = [&](int used, auto &&look) {
-        const int64_t all = int64_t(used) * chunks, end = all * (wave + 1) / kDownWaves;
-        int64_t u = all * wave / kDownWaves;
+        const int64_t all = int64_t(used) * chunks;
+        const int part = int(blockIdx.z) * kDownWaves + wave, parts = from.splits * kDownWaves;
+        const int64_t end = all * (part + 1) / parts;
+        int64_t u = all * part / parts;
         int a = int(u / chunks);
         Work next{};
         if (u < end) next = look(a);
@@ -427,15 +461,53 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
         });
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < count * 4; i += 64 * kDownWaves) {
-        f32x4 sum = sums[i];
-#pragma unroll
-        for (int v = 1; v < kDownWaves; ++v) sum += sums[v * count * 4 + i];
+    auto store = [&](int i, f32x4 sum) {
         const int c = n0 + 4 * (i & 3);
         X *o = out + int64_t(t0 + i / 4) * ld_out + c;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (c + e < width) o[e] = rounded<X>(sum[e]);
+    };
+    // Parts of other blocks' sums: stores and loads of agent scope, past the caches of the compute dies. (Plain ones
+    // between fences of that scope, which write a die's whole cache back, took 60 us more.)
+    using Pair = uint64_t __attribute__((ext_vector_type(2)));
+    auto part_of = [&](int z, int i) {
+        return reinterpret_cast<uint64_t *>(from.parts) +
+               (((int64_t(z) * ch.tokens + t0 + i / 4) * from.tiles + blockIdx.x) * 4 + (i & 3)) * 2;
+    };
+    auto load_part = [&](int z, int i) {
+        uint64_t *p = part_of(z, i);
+        Pair v;
+        v[0] = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        v[1] = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return bits_as<f32x4>(v);
+    };
+    for (int i = threadIdx.x; i < count * 4; i += 64 * kDownWaves) {
+        f32x4 sum = sums[i];
+#pragma unroll
+        for (int v = 1; v < kDownWaves; ++v) sum += sums[v * count * 4 + i];
+        if (from.splits == 1) store(i, sum);
+        else {
+            uint64_t *p = part_of(blockIdx.z, i);
+            const Pair v = bits_as<Pair>(sum);
+            __hip_atomic_store(p, v[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(p + 1, v[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+    if (from.splits == 1) return;
+    // the last block to come adds all parts, in their order: each wave's stores are acknowledged before the barrier
+    __shared__ int s_last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = __hip_atomic_fetch_add(&from.arrived[group * from.tiles + int(blockIdx.x)], 1, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT) == from.splits - 1;
+    __syncthreads();
+    if (!s_last) return;
+    for (int i = threadIdx.x; i < count * 4; i += 64 * kDownWaves) {
+        f32x4 sum = load_part(0, i);
+        for (int z = 1; z < from.splits; ++z) sum += load_part(z, i);
+        store(i, sum);
     }
 }
 
@@ -445,7 +517,15 @@ __global__ __launch_bounds__(256) void k_zero_out(ZeroRows z) { z.run(0); }
 
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
-size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, void *ws, Between *to) {
+// How many blocks share 16 columns of the result: so many that there are two for each compute unit, while each wave
+// has two chunks of hidden units if all choices are of different experts.
+int splits(int64_t tokens, int64_t top_k, int64_t experts, int64_t width, int64_t hidden) {
+    const int64_t blocks = (width + 15) / 16 * ((tokens + kGroup - 1) / kGroup);
+    const int64_t work = std::min(tokens * top_k, experts) * ((hidden + kChunkK - 1) / kChunkK);
+    return int(std::max<int64_t>(1, std::min({int64_t(kSplitsMax), 511 / blocks, work / (2 * kDownWaves)})));
+}
+
+size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t width, int64_t hidden, void *ws, Between *to) {
     const int64_t slots = tokens * top_k, most = std::min(slots, experts);
     const int64_t padded = (hidden + kChunkK - 1) / kChunkK * kChunkK;
     char *p = static_cast<char *>(ws);
@@ -459,7 +539,14 @@ size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t hidden, voi
     char *count = take(4), *expert = take(size_t(most) * 4), *counts = take(size_t(most * groups) * 4);
     char *list = take(size_t(most * groups) * kGroup * 8);
     char *hi = take(size_t(slots) * size_t(padded) * 2), *lo = take(size_t(slots) * size_t(padded) * 2);
+    const int64_t tiles = (width + 15) / 16, n = splits(tokens, top_k, experts, width, hidden);
+    char *parts = take(n > 1 ? size_t(n * tokens * tiles) * 64 : 0);
+    char *arrived = take(n > 1 ? size_t(groups * tiles) * 4 : 0);
     if (to) {
+        to->parts = reinterpret_cast<float *>(parts);
+        to->arrived = reinterpret_cast<int *>(arrived);
+        to->tiles = int(tiles);
+        to->splits = int(n);
         to->count = reinterpret_cast<int *>(count);
         to->expert = reinterpret_cast<int *>(expert);
         to->counts = reinterpret_cast<int *>(counts);
@@ -492,25 +579,36 @@ void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matr
             hipStream_t s) {
     const int tiles = (hidden + 15) / 16, most = std::min(ch.tokens * ch.top_k, ch.experts);
     const bool few = ch.tokens <= 16 && ch.tokens * ch.top_k <= 64;
+    const int chunks = (width + kChunkK - 1) / kChunkK;
+    const size_t lds = size_t(ch.tokens) * staged_row(width) * 2;
+    const bool stage = lds <= kStageMax;
+    int log_share = kLogWaves;  // tokens too wide to be staged have chunks for all waves, or nearly
+    while (log_share > 0 && chunks < 2 << log_share && !(few && !stage)) --log_share;
+    const bool all = log_share == kLogWaves;
+    const int64_t up_blocks = ((int64_t(tiles) << log_share) + kUpWaves - 1) / kUpWaves;
     if (few) {
-        auto go = [&](auto stage, size_t lds) {
-            hipLaunchKernelGGL((k_experts_up_few<W, X, GELU, decltype(stage)::value>), dim3(tiles, most),
-                               dim3(64 * kUpWaves), lds, s, ch, x, ld_x, matrix<W>(gate), matrix<W>(up), width, hidden,
-                               b);
+        auto go = [&](auto stage, auto by_all, size_t lds) {
+            hipLaunchKernelGGL((k_experts_up_few<W, X, GELU, decltype(stage)::value, decltype(by_all)::value>), dim3(unsigned(up_blocks), most), dim3(64 * kUpWaves), lds, s, ch, x, ld_x,
+                               matrix<W>(gate), matrix<W>(up), width, hidden, log_share, b);
         };
-        const size_t lds = size_t(ch.tokens) * staged_row(width) * 2;
-        if (lds <= kStageMax) go(std::true_type{}, lds);
-        else go(std::false_type{}, 0);
+        if (stage && all) go(std::true_type{}, std::true_type{}, lds);
+        else if (stage) go(std::true_type{}, std::false_type{}, lds);
+        else go(std::false_type{}, std::true_type{}, 0);
     } else {
         // a block builds its expert's list once for up to four runs of hidden units, while there are blocks for all
-        const int own = std::max(1, std::min(4, int(int64_t(tiles) * most / 1024)));
-        const dim3 grid((tiles + own - 1) / own, most);
-        auto go = [&](auto mt) {
-            hipLaunchKernelGGL((k_experts_up<W, X, GELU, decltype(mt)::value>), grid, dim3(64 * kUpWaves), 0, s, ch, x,
-                               ld_x, matrix<W>(gate), matrix<W>(up), width, hidden, own, b);
+        const int own = std::max(1, std::min(4, int(up_blocks * most / 1024)));
+        const dim3 grid(unsigned((up_blocks + own - 1) / own), most);
+        auto go = [&](auto mt, auto by_all) {
+            hipLaunchKernelGGL((k_experts_up<W, X, GELU, decltype(mt)::value, decltype(by_all)::value>), grid, dim3(64 * kUpWaves), 0, s, ch, x,
+                               ld_x, matrix<W>(gate), matrix<W>(up), width, hidden, log_share, own, b);
         };
-        if (ch.tokens <= 16) go(std::integral_constant<int, 1>{});
-        else go(std::integral_constant<int, 4>{});
+        auto with_tiles = [&](auto by_all) {
+            if (ch.tokens <= 16) go(std::integral_constant<int, 1>{}, by_all);
+            else go(std::integral_constant<int, 4>{}, by_all);
+        };
+        // (4-bit rows need more registers than there are with the constant)
+        if (std::is_same_v<W, Mx4> || !all) with_tiles(std::false_type{});
+        else if constexpr (!std::is_same_v<W, Mx4>) with_tiles(std::true_type{});
     }
     auto go = [&](auto mt, auto by_few, auto stage, size_t staged) {
         constexpr int MT = decltype(mt)::value;
@@ -518,7 +616,7 @@ void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matr
         const size_t lds = size_t(kDownWaves) * std::min(ch.tokens, kGroup) * 64 + staged;
         allow_lds<&k_experts_down<W, X, MT, FEW, STAGE>>(size_t(kDownWaves) * 16 * 64 + (STAGE ? 2 * kStageMax : 0));
         hipLaunchKernelGGL((k_experts_down<W, X, MT, FEW, STAGE>),
-                           dim3((width + 15) / 16, (ch.tokens + kGroup - 1) / kGroup), dim3(64 * kDownWaves), lds, s, ch,
+                           dim3(b.tiles, b.groups, b.splits), dim3(64 * kDownWaves), lds, s, ch,
                            b, matrix<W>(down), hidden, width, out, ld_out);
     };
     constexpr std::integral_constant<int, 1> one{};
@@ -538,7 +636,7 @@ vspmm_status vspmm_expert_mlp_workspace_size(int64_t n_tokens, int64_t top_k, in
     if (!bytes) return VSPMM_ERR_NULL;
     if (vspmm_status st = check_extents(n_tokens, top_k, n_experts, width, hidden)) return st;
     const bool none = n_tokens == 0 || top_k == 0 || n_experts == 0 || width == 0 || hidden == 0;
-    *bytes = none ? 0 : carve(n_tokens, top_k, n_experts, hidden, nullptr, nullptr);
+    *bytes = none ? 0 : carve(n_tokens, top_k, n_experts, width, hidden, nullptr, nullptr);
     return VSPMM_OK;
 }
 
@@ -574,7 +672,7 @@ vspmm_status vspmm_expert_mlp(vspmm_elt elt, vspmm_elt weights_elt, vspmm_index 
             return launched();
         }
         Between b;
-        carve(n_tokens, top_k, n_experts, hidden, ws, &b);
+        carve(n_tokens, top_k, n_experts, width, hidden, ws, &b);
         const Choices ch{experts, index == VSPMM_INDEX_I64, weight, int(n_tokens), int(top_k), int(n_experts)};
         auto go = [&](auto w, auto gelu) {
             launch<decltype(w), T, decltype(gelu)::value>(ch, static_cast<const T *>(x), ld_x, *gate, *up, *down,

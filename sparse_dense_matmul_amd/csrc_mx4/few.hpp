@@ -292,7 +292,7 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
         }
     } else {
         // blocks of 32 one after another, or, where registers allow, all loaded first; those past the end are zeros
-        constexpr int N = MT == 1 ? kChunkK / kBlock : 1;
+        constexpr int N = MT > 1 ? 1 : CODES || R == 1 ? kChunkK / kBlock : 2;
 #pragma unroll 1
         for (int k0 = c * kChunkK; k0 < width; k0 += N * kBlock) {
             i32x4 a[N][R];
