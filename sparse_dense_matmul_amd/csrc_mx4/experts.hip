@@ -2,11 +2,15 @@
 // weighted and summed. Declared in include/vspmm.h.
 //
 // The work is reading the weights of every expert that a token is sent to, once. The first launch takes 16 hidden
-// units of one expert a block (a block finds its expert, the a-th of those in use, and its tokens in the list of
-// choices by itself) and writes act(gate x) (up x) times the router's weight. The second takes 16 columns of the result a block and
-// sums over all experts in use, so that no sum crosses blocks: its order is fixed, and no third launch joins parts.
-// Hidden values go between them as the sum of two bfloat16 numbers (17 bits, for float32's 24: far under the result's
-// rounding), which the second launch's matrix instructions take as they are.
+// units of one expert for all its tokens (a block finds its expert, the a-th of those in use, and its tokens in the
+// list of choices by itself) and writes act(gate x) (up x) times the router's weight. The second takes 16 columns of
+// the result a block and sums over all experts in use; where there are few columns several blocks share them and the
+// last adds their parts, in order. Every sum's order is fixed. Hidden values go between the launches as the sum of two
+// bfloat16 numbers (17 bits, for float32's 24: far under the result's rounding), which the second launch's matrix
+// instructions take as they are.
+//
+// 64 tokens to 8 of 128 experts of 4,096 x 1,024, bfloat16: 417 and 235 us, 4.9 TB/s of weights. One token, 4 bits: 13
+// and 9 us, latency: 7.5 us of bytes.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -29,7 +29,8 @@ __device__ __forceinline__ uint32_t encode(const float (&v)[8], uint32_t scale) 
 }
 
 // A lane takes 8 values of a row, four lanes a block: 16-byte loads of 16-bit values and 4-byte stores of codes, both
-// without gaps over the lanes. per_row: lanes of a row, 4 * blocks.
+// without gaps over the lanes. Bound by memory, and at a few rows by the launch (32 x 4,096 bfloat16: 2.6 us). per_row:
+// lanes of a row, 4 * blocks.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize(const T *__restrict__ x, int64_t ld, uint32_t n, FastDiv by_row,
                                                   uint32_t per_row, int width, uint8_t *__restrict__ codes,
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(256) void k_quantize(const T *__restrict__ x, int64
 
 // The transpose's rows: a lane takes two columns of x over the 32 rows of one of their blocks, so a wave reads 128
 // columns in a row. Eight waves take eight blocks in a row of the same columns, whose codes meet in LDS and leave as
-// 128 bytes a column.
+// 128 bytes a column. Bound by memory: 16,384 x 8,192 bfloat16 in 72 to 93 us, 3.6 to 4.7 TB/s.
 constexpr int kTransposeWaves = 8, kTransposeCols = 128;
 template <typename T>
 __global__ __launch_bounds__(64 * kTransposeWaves) void k_quantize_transposed(
@@ -116,7 +117,8 @@ __global__ __launch_bounds__(64 * kTransposeWaves) void k_quantize_transposed(
     }
 }
 
-// A lane takes 8 codes: 4-byte loads, 16-byte stores of 16-bit values.
+// A lane takes 8 codes: 4-byte loads, 16-byte stores of 16-bit values. Bound by memory: 8,192 x 16,384 to bfloat16 in
+// 68 us, 5.0 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_dequantize(const uint8_t *__restrict__ codes, int64_t ld_codes,
                                                     const uint8_t *__restrict__ scales, int64_t ld_scales, uint32_t n,
