@@ -87,9 +87,14 @@ vspmm_status zero_rows(O *out, int64_t ld, int64_t rows, int64_t width, hipStrea
 // Tiles of a product past one launch are of more than 2^43 results.
 bool too_many(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) / 64) > kI32Max; }
 
-// Up to this many tokens the few-token kernel, which reads the tokens once for 32 rows; tiles beyond (4,096 x 4,096:
-// 32 tokens 13 us by the one, 19 by the other, 64 tokens 21 and 18).
+// The few-token kernel, which reads the tokens once for 32 rows, takes up to 32 tokens, and dense ones up to 64 where its
+// blocks of 32 x 32 find a compute unit each (64 tokens through 4,096 x 4,096: 12.4 us, by tiles 17.6; 2,048 x 8,192: 23
+// and 29; through 5,003 x 4,001 rows, past that, 37 tokens 29 to 36 and 22 to 25). Tiles beyond. With both sides in 4 bits
+// tiles are as fast from 33 on (2,048 x 8,192: 12.4 us, 16.5 by this kernel).
 constexpr int64_t kFewTokens = 32;
+bool few_dense_tokens(int64_t m, int64_t n) {
+    return m <= kFewTokens || (m <= 2 * kFewTokens && ((m + 31) / 32) * ((n + 31) / 32) <= 256);
+}
 
 template <typename X, typename O>
 void launch_few(Row<X> x, int64_t ld_x, int64_t ld_xs, const vspmm_mx4 &w, O *out, int64_t ld_out, int m, int n, int k,
@@ -212,7 +217,7 @@ vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width
         using T = decltype(e);
         T *o = static_cast<T *>(out);
         if (width == 0) return zero_rows(o, ld_out, m, n, stream);
-        if (m <= kFewTokens) {
+        if (few_dense_tokens(m, n)) {
             launch_few(Row<T>{static_cast<const T *>(x)}, ld_x, 0, *w, o, ld_out, int(m), int(n), int(width), stream);
             return launched();
         }
