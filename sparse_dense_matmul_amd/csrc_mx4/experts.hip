@@ -5,9 +5,8 @@
 // units of one expert for all its tokens (a block finds its expert, the a-th of those in use, and its tokens in the
 // list of choices by itself) and writes act(gate x) (up x) times the router's weight. The second takes 16 columns of
 // the result a block and sums over all experts in use; where there are few columns several blocks share them and the
-// last adds their parts, in order. Every sum's order is fixed. Hidden values go between the launches as the sum of two
-// bfloat16 numbers (17 bits, for float32's 24: far under the result's rounding), which the second launch's matrix
-// instructions take as they are.
+// last adds their parts, in order. Every sum's order is fixed. Hidden values go between the launches as the sum of three
+// bfloat16 numbers, which hold float32's 24 bits and which the second launch's matrix instructions take as they are.
 //
 // 64 tokens to 8 of 128 experts of 4,096 x 1,024, bfloat16: 417 and 235 us, 4.9 TB/s of weights. One token, 4 bits: 13
 // and 9 us, latency: 7.5 us of bytes.
@@ -54,7 +53,7 @@ struct Between {
     int *count, *expert;  // [1], [most]
     int *counts;          // [most, groups]
     int2 *list;           // [most, groups, kGroup]: token, slot
-    bf16 *hi, *lo;        // [slots, padded]
+    bf16 *hidden;         // [slots, padded / 8, part, 8]
     int64_t padded;
     int groups;
     // of a result whose experts are split over blocks: the parts, [splits, tokens, tiles, 16], and how many have come
@@ -138,22 +137,28 @@ __device__ __forceinline__ void store_hidden(const f32x4 (*parts)[2][64], int wa
         for (int i = 0; i < 4; ++i) sg[i] += v < waves ? a[i] : 0.0f, su[i] += v < waves ? b[i] : 0.0f;
     }
     const int f = f0 + 4 * (lane >> 4);
-    const int64_t base = slot * to.padded + f;
-    bf16x4 hi, lo;
+    bf16 *row = to.hidden + at_planes(slot * to.padded);
+    bf16x4 hi, mid, lo;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float h = f + i < hidden ? weight * (activate<GELU>(sg[i]) * su[i]) : 0.0f;
-        hi[i] = bf16(h);
-        // an infinity has no second part
-        lo[i] = __builtin_isinf(float(hi[i])) ? bf16(0.0f) : bf16(h - float(hi[i]));
+        // Eight bits of the significand, the next eight and the last, each with h's sign: exact down to bfloat16's least
+        // number, 2^-133. An infinity or NaN has the first part alone.
+        const float top = __uint_as_float(__float_as_uint(h) & 0xffff0000u), rest = __builtin_isfinite(h) ? h - top : 0.0f;
+        const float next = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+        hi[i] = bf16(top);
+        mid[i] = bf16(next);
+        lo[i] = bf16(rest - next);
     }
-    *reinterpret_cast<bf16x4 *>(to.hi + base) = hi;
-    *reinterpret_cast<bf16x4 *>(to.lo + base) = lo;
+    const auto store = [&](int64_t k, bf16x4 a, bf16x4 b, bf16x4 c) {
+        bf16 *p = row + at_planes(k & ~int64_t(7)) + (k & 7);
+        *reinterpret_cast<bf16x4 *>(p) = a;
+        *reinterpret_cast<bf16x4 *>(p + 8) = b;
+        *reinterpret_cast<bf16x4 *>(p + 16) = c;
+    };
+    store(f, hi, mid, lo);
     if (f0 + 16 >= hidden)  // zeros to the end of the last chunk
-        for (int64_t i = 16; f + i < to.padded; i += 16) {
-            *reinterpret_cast<bf16x4 *>(to.hi + base + i) = bf16x4{};
-            *reinterpret_cast<bf16x4 *>(to.lo + base + i) = bf16x4{};
-        }
+        for (int64_t k = f + 16; k < to.padded; k += 16) store(k, bf16x4{}, bf16x4{}, bf16x4{});
 }
 
 // 4-bit rows and float16 tokens, multiplied in either type, need more than the 128 registers that let two blocks share a
@@ -302,6 +307,7 @@ __global__ __launch_bounds__(64 * kUpWaves, (MT == 1 && !kWide<W, X> ? 4 : 1)) v
 
 // A row of staged tokens: whole chunks, and 16 bytes so that the rows' starts lie in different banks.
 __host__ __device__ constexpr int staged_row(int width) { return (width + kChunkK - 1) / kChunkK * kChunkK + 8; }
+__host__ __device__ constexpr int staged_planes(int width) { return 3 * ((width + kChunkK - 1) / kChunkK * kChunkK) + 8; }
 
 // The same with few choices: no list is built, and the weights are under way after one load. STAGE: the expert's tokens
 // go to LDS first.
@@ -376,16 +382,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
     f32x4 *own = sums + wave * count * 4;
     for (int i = lane; i < count * 4; i += 64) own[i] = f32x4{};
     using H = std::conditional_t<STAGE, Staged<Planes>, Planes>;
+    // chunks on their way at once: one of hidden values and 16-bit weights takes 64 registers
+    constexpr int AT_ONCE = !STAGE ? (std::is_same_v<W, Mx4> ? 2 : 1) : std::is_same_v<W, f16> ? 2 : 4;
     bf16 *staged = reinterpret_cast<bf16 *>(sums + kDownWaves * count * 4);
-    const int slots = ch.tokens * ch.top_k, row = staged_row(hidden), lds_lo = slots * row;
+    const int slots = ch.tokens * ch.top_k, row = staged_planes(hidden);
     if constexpr (STAGE) {
-        const int per_row = int(from.padded) / 8;
+        const int per_row = 3 * int(from.padded) / 8;
         for (int i = threadIdx.x; i < slots * per_row; i += 64 * kDownWaves) {
             const int s = i / per_row, k = (i - s * per_row) * 8;
             *reinterpret_cast<i32x4 *>(staged + s * row + k) =
-                *reinterpret_cast<const i32x4 *>(from.hi + s * from.padded + k);
-            *reinterpret_cast<i32x4 *>(staged + lds_lo + s * row + k) =
-                *reinterpret_cast<const i32x4 *>(from.lo + s * from.padded + k);
+                *reinterpret_cast<const i32x4 *>(from.hidden + at_planes(s * from.padded) + k);
         }
         lds_barrier();
     }
@@ -424,11 +430,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
                     token[m] = entry.x;
                     live[m] = first + 16 * m + r < now.tokens;
                     if constexpr (STAGE) {
-                        const LdsPtr<bf16> at = (LdsPtr<bf16>)(staged) + (live[m] ? entry.y : 0) * row;
-                        x[m] = {at, at + lds_lo};
+                        x[m] = {(LdsPtr<bf16>)(staged) + (live[m] ? entry.y : 0) * row};
                     } else {
-                        const int64_t base = (live[m] ? entry.y : 0) * from.padded;
-                        x[m] = {from.hi + base, from.lo + base};
+                        x[m] = {from.hidden + at_planes((live[m] ? entry.y : 0) * from.padded), live[m]};
                     }
                 }
                 f32x4 part[1][N] = {};
@@ -441,7 +445,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
             for (int first = 0; first < now.tokens; first += 16 * MT) {
                 if (MT > 1 && now.tokens - first > 16)
                     pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
-                else pass(integral_constant<int, 1>{}, integral_constant<int, (std::is_same_v<W, f16> ? 2 : 4)>{}, first);
+                else pass(integral_constant<int, 1>{}, integral_constant<int, AT_ONCE>{}, first);
             }
         }
     };
@@ -542,7 +546,7 @@ size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t width, int6
     const int64_t groups = (tokens + kGroup - 1) / kGroup;
     char *count = take(4), *expert = take(size_t(most) * 4), *counts = take(size_t(most * groups) * 4);
     char *list = take(size_t(most * groups) * kGroup * 8);
-    char *hi = take(size_t(slots) * size_t(padded) * 2), *lo = take(size_t(slots) * size_t(padded) * 2);
+    char *values = take(size_t(slots) * size_t(padded) * 6);
     const int64_t tiles = (width + 15) / 16, n = splits(tokens, top_k, experts, width, hidden);
     char *parts = take(n > 1 ? size_t(n * tokens * tiles) * 64 : 0);
     char *arrived = take(n > 1 ? size_t(groups * tiles) * 4 : 0);
@@ -555,8 +559,7 @@ size_t carve(int64_t tokens, int64_t top_k, int64_t experts, int64_t width, int6
         to->expert = reinterpret_cast<int *>(expert);
         to->counts = reinterpret_cast<int *>(counts);
         to->list = reinterpret_cast<int2 *>(list);
-        to->hi = reinterpret_cast<bf16 *>(hi);
-        to->lo = reinterpret_cast<bf16 *>(lo);
+        to->hidden = reinterpret_cast<bf16 *>(values);
         to->padded = padded;
         to->groups = int(groups);
     }
@@ -624,7 +627,7 @@ void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matr
                            b, matrix<W>(down), hidden, width, out, ld_out);
     };
     constexpr std::integral_constant<int, 1> one{};
-    const size_t staged = size_t(ch.tokens) * ch.top_k * staged_row(hidden) * 4;
+    const size_t staged = size_t(ch.tokens) * ch.top_k * staged_planes(hidden) * 2;
     if (few && staged <= 2 * kStageMax) go(one, std::true_type{}, std::true_type{}, staged);
     else if (few) go(one, std::true_type{}, std::false_type{}, 0);
     else if (ch.tokens <= 16) go(one, std::false_type{}, std::false_type{}, 0);

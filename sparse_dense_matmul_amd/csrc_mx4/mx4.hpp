@@ -34,7 +34,7 @@ using Half16 = i32x4 __attribute__((aligned(2)));
 using Byte16 = i32x4 __attribute__((aligned(1)));
 
 struct Mx4 {};     // element type of a microscaled matrix
-struct Planes {};  // float32 values as the sum of two bfloat16 ones, each in an array of its own
+struct Planes {};  // float32 values as the sum of three bfloat16 ones, eight values' first, second and third parts in turn
 
 template <typename T, typename F>
 __device__ __forceinline__ T bits_as(F x) {
