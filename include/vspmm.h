@@ -683,8 +683,10 @@ typedef enum { VSPMM_SILU = 0, VSPMM_GELU = 1 } vspmm_activation;
  * outside [0, n_experts) adds nothing, and only the weights of experts that some
  * token chose are read. weight: device float32 [n_tokens, top_k]. act: x / (1 +
  * exp(-x)), or x / 2 (1 + erf(x / sqrt 2)). Sums, activations
- * and hidden values, which take the token's weight, are in float32 (what a hidden
- * value has under 2^-133 is lost). A token's result does not depend on the
+ * and hidden values, which take the token's weight (the sum of its weights where
+ * it chose an expert more than once), are in float32 (what a hidden value has
+ * under 2^-133 is lost). An infinite or NaN weight, 4-bit value or hidden value
+ * gives what float32 products with it give. A token's result does not depend on the
  * others' values. More tokens: vspmm_route, vspmm_dispatch, a product per expert
  * and vspmm_combine. ws: vspmm_expert_mlp_workspace_size bytes. Errors: _NULL,
  * _DIM, _ENUM, _WORKSPACE, _UNSUPPORTED (more than 1,024 tokens, 4,096 experts or

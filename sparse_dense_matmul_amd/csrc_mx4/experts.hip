@@ -414,6 +414,18 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
             u += c1 - c0;
             if (u < end) next = look(a + 1);  // loaded while this one is multiplied
             const Row<W> rows[1] = {down.row(now.expert, n)};
+            // the lane's token and slot in a tile of the expert's tokens
+            const auto entry_of = [&](int at) {
+                int2 entry = make_int2(now.token, now.slot);
+                if (!FEW && at > 0)
+                    entry = from.list[(int64_t(a) * from.groups + group) * kGroup + min(at + r, now.tokens - 1)];
+                return entry;
+            };
+            const auto hidden_of = [&](bool live, int slot) -> Row<H> {
+                if constexpr (STAGE) return {(LdsPtr<bf16>)(staged) + (live ? slot : 0) * row};
+                else return {from.hidden + at_planes((live ? slot : 0) * from.padded), live};
+            };
+            // which of N tiles from `first` on have to be done again
             auto pass = [&](auto mt, auto in_flight, int first) {
                 constexpr int N = decltype(mt)::value;
                 Row<H> x[N];
@@ -421,31 +433,41 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
                 bool live[N];
 #pragma unroll
                 for (int m = 0; m < N; ++m) {
-                    int2 entry = make_int2(now.token, now.slot);
-                    if constexpr (N > 1)
-                        entry = from.list[(int64_t(a) * from.groups + group) * kGroup +
-                                          min(first + 16 * m + r, now.tokens - 1)];
-                    else if (!FEW && first > 0)
-                        entry = from.list[(int64_t(a) * from.groups + group) * kGroup + min(first + r, now.tokens - 1)];
+                    const int2 entry = entry_of(first + 16 * m);
                     token[m] = entry.x;
                     live[m] = first + 16 * m + r < now.tokens;
-                    if constexpr (STAGE) {
-                        x[m] = {(LdsPtr<bf16>)(staged) + (live[m] ? entry.y : 0) * row};
-                    } else {
-                        x[m] = {from.hidden + at_planes((live[m] ? entry.y : 0) * from.padded), live[m]};
-                    }
+                    x[m] = hidden_of(live[m], entry.y);
                 }
                 f32x4 part[1][N] = {};
                 accumulate<decltype(in_flight)::value>(part, rows, x, c0, c1, hidden, g);
+                uint32_t again = 0;
 #pragma unroll
-                for (int m = 0; m < N; ++m)
-                    if (live[m]) own[(token[m] - t0) * 4 + g] += part[0][m];
+                for (int m = 0; m < N; ++m) {
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) nan = nan || __builtin_isnan(part[0][m][i]);
+                    if (__any(live[m] && nan)) again |= 1u << m;
+                    else if (live[m]) own[(token[m] - t0) * 4 + g] += part[0][m];
+                }
+                return again;
             };
             using std::integral_constant;
             for (int first = 0; first < now.tokens; first += 16 * MT) {
+                uint32_t again;
                 if (MT > 1 && now.tokens - first > 16)
-                    pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
-                else pass(integral_constant<int, 1>{}, integral_constant<int, AT_ONCE>{}, first);
+                    again = pass(integral_constant<int, MT>{}, integral_constant<int, 1>{}, first);
+                else again = pass(integral_constant<int, 1>{}, integral_constant<int, AT_ONCE>{}, first);
+                // An infinite weight times a hidden value's parts is rightly infinite (all have the value's sign), or NaN if
+                // a later part is zero; so is an infinite hidden value times a weight's. Rare: done again with care.
+                for (; again; again &= again - 1) {
+                    const int at = first + 16 * __builtin_ctz(again);
+                    const bool live = at + r < now.tokens;
+                    const int2 entry = entry_of(at);
+                    const Row<H> x[1] = {hidden_of(live, entry.y)};
+                    f32x4 part[1][1] = {};
+                    accumulate<1, true>(part, rows, x, c0, c1, hidden, g);
+                    if (live) own[(entry.x - t0) * 4 + g] += part[0][0];
+                }
             }
         }
     };

@@ -149,8 +149,8 @@ __device__ __forceinline__ float scale_operand_of(uint32_t scales, int j) {
 }
 
 // One instruction's worth of a matrix's rows, a (of type T: its own, or what its codes were widened to), and a token
-// tile: as many instructions as the two have parts.
-template <typename T, typename X>
+// tile: as many instructions as the two have parts. CAREFUL: a factor in parts may meet infinities.
+template <typename T, bool CAREFUL, typename X>
 __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 c) {
     using V = typename Plain<X>::type;
     if constexpr (std::is_same_v<V, T>) {
@@ -159,10 +159,11 @@ __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 
         i32x4 hi = a, lo;
         if constexpr (std::is_same_v<T, f16>) split(a, hi, lo);
         c = mma16<bf16>(hi, x.hi, c);
+        if constexpr (CAREFUL) hi = finite(hi);
         c = mma16<bf16>(hi, x.mid, c);
         c = mma16<bf16>(hi, x.lo, c);
         if constexpr (std::is_same_v<T, f16>) {
-            c = mma16<bf16>(lo, x.hi, c);
+            c = mma16<bf16>(lo, CAREFUL ? finite(x.hi) : x.hi, c);
             c = mma16<bf16>(lo, x.mid, c);
             c = mma16<bf16>(lo, x.lo, c);
         }
@@ -180,14 +181,14 @@ __device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) { return _
 
 // acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values, U at a time. One tile's tokens are
 // loaded by chunks; those of several, which would need more registers than there are, and those in LDS beside the
-// products.
-template <int U, typename W, typename X, int R, int MT>
+// products. CAREFUL: see multiply_step; all of the range goes by blocks of 32, in few registers.
+template <int U, bool CAREFUL = false, typename W, typename X, int R, int MT>
 __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&rows)[R], const Row<X> (&x)[MT], int c0,
                                            int c1, int width, int g) {
     constexpr bool BOTH = std::is_same_v<X, Mx4>, CODES = std::is_same_v<W, Mx4>;
     constexpr bool BY_CHUNKS = BOTH || (MT == 1 && !Plain<X>::staged);
     using V = typename Plain<X>::type;
-    const int whole = min(width / kChunkK, c1);
+    const int whole = CAREFUL ? c0 : min(width / kChunkK, c1);
     int c = c0;
     // N chunks: all are on their way before the first is waited for, as far as the compiler leaves it so
     auto load_rows = [&](auto &w, int at) {
@@ -251,7 +252,7 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
                         else if constexpr (std::is_same_v<V, Planes>) s = {t[m].hi[j], t[m].mid[j], t[m].lo[j]};
                         else s.hi = t[m].v[j];
 #pragma unroll
-                        for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[i], s, acc[i][m]);
+                        for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T, CAREFUL>(a[i], s, acc[i][m]);
                     }
                 }
             };
@@ -280,11 +281,13 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
         for (int u = 0; u < N; ++u) multiply(w[u], t[u], c + u);
         c += N;
     };
-    while (c + U <= whole) some(std::integral_constant<int, U>{});
-    if constexpr (U > 2)
-        if (c + 2 <= whole) some(std::integral_constant<int, 2>{});
-    if constexpr (U > 1)
-        if (c < whole) some(std::integral_constant<int, 1>{});
+    if constexpr (!CAREFUL) {
+        while (c + U <= whole) some(std::integral_constant<int, U>{});
+        if constexpr (U > 2)
+            if (c + 2 <= whole) some(std::integral_constant<int, 2>{});
+        if constexpr (U > 1)
+            if (c < whole) some(std::integral_constant<int, 1>{});
+    }
     if (c >= c1) {
         settle(acc);
         return;
@@ -311,10 +314,11 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
             for (int i = 0; i < R; ++i) acc[i][m] = mma16_mx4<0>(w[i].codes, w[i].scale, t.codes, t.scale, acc[i][m]);
         }
     } else {
-        // blocks of 32 one after another, or, where registers allow, all loaded first; those past the end are zeros
-        constexpr int N = MT > 1 ? 1 : CODES || R == 1 ? kChunkK / kBlock : 2;
+        // blocks of 32 one after another, or, where registers allow, two or all loaded first; those past the end are zeros
+        constexpr int N = CAREFUL || MT > 1 ? 1 : CODES ? kChunkK / kBlock : 2;
+        const int end = CAREFUL ? min(width, c1 * kChunkK) : width;
 #pragma unroll 1
-        for (int k0 = c * kChunkK; k0 < width; k0 += N * kBlock) {
+        for (int k0 = c * kChunkK; k0 < end; k0 += N * kBlock) {
             i32x4 a[N][R];
             uint32_t word[N][R], top[N][R];
             Step<X> s[N][MT];
@@ -373,7 +377,7 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T>(a[n][i], s[n][m], acc[i][m]);
+                        for (int i = 0; i < R; ++i) acc[i][m] = multiply_step<T, CAREFUL>(a[n][i], s[n][m], acc[i][m]);
                 }
             };
             if constexpr (!CODES) {

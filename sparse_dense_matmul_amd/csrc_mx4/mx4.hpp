@@ -88,6 +88,19 @@ __device__ __forceinline__ void split(i32x4 v, i32x4 &hi, i32x4 &lo) {
     }
 }
 
+// Eight bfloat16 values, zeros in the place of infinities and NaN. Where a factor goes in parts, an infinity of the other
+// meets the first part alone: the others may be zero, and infinity times zero is not a number.
+__device__ __forceinline__ i32x4 finite(i32x4 v) {
+    i32x4 out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = uint32_t(v[i]);
+        const uint32_t top = ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // of a half: its exponent is the largest
+        out[i] = int32_t(w & ~(top - (top >> 15)));
+    }
+    return out;
+}
+
 template <typename T>
 __device__ __forceinline__ f32x4 mma16(i32x4 a, i32x4 b, f32x4 c) {
     if constexpr (std::is_same_v<T, bf16>)
