@@ -172,7 +172,8 @@ __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 
         i32x4 hi, lo;
         split(x.hi, hi, lo);
         c = mma16<bf16>(a, hi, c);
-        return mma16<bf16>(a, lo, c);
+        asm volatile("" : "+v"(a));  // found anew for each tile of tokens, not kept in registers between
+        return mma16<bf16>(finite(a), lo, c);
     }
 }
 

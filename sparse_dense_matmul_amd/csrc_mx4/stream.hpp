@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
                     acc[i][j] = mma32<T>(p[set][i], hi, acc[i][j]);
-                    if constexpr (!std::is_same_v<T, X>) acc[i][j] = mma32<T>(p[set][i], lo, acc[i][j]);
+                    if constexpr (!std::is_same_v<T, X>) acc[i][j] = mma32<T>(finite(p[set][i]), lo, acc[i][j]);
                 }
             }
         };
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(256, 1) void k_stream_grad(const X *__restrict__ dy
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
                     acc[i][j] = mma32<T>(p[set][i], hi, acc[i][j]);
-                    if constexpr (!std::is_same_v<T, X>) acc[i][j] = mma32<T>(p[set][i], lo, acc[i][j]);
+                    if constexpr (!std::is_same_v<T, X>) acc[i][j] = mma32<T>(finite(p[set][i]), lo, acc[i][j]);
                 }
             }
         };

@@ -213,7 +213,9 @@ __device__ __forceinline__ void multiply_tiles(f32x16 (&acc)[TW][TW], const i32x
 #pragma unroll
             for (int i = 0; i < TW; ++i) {
                 acc[i][j] = mma32<bf16>(p[i], hi, acc[i][j]);
-                acc[i][j] = mma32<bf16>(p[i], lo, acc[i][j]);
+                i32x4 rows = p[i];
+                asm volatile("" : "+v"(rows));  // found anew for each j, not kept in registers between
+                acc[i][j] = mma32<bf16>(finite(rows), lo, acc[i][j]);
             }
         } else {
 #pragma unroll
