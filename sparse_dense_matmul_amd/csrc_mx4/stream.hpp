@@ -219,7 +219,10 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
     const int r = lane & 31, g = lane >> 5;
     uint32_t tm, tn;
     tile_of(s, (uint32_t(s.m) + 255) / 256, tm, tn);
-    const int m0 = min(int(tm) * 256, s.m - 256), n0 = min(int(tn) * 256, s.n - 256);
+    // The last tile of either side is moved to end with the matrix. Columns stay those of the tile that they would lie in:
+    // the route of float16 tokens is chosen by a tile's own rows, and the two tiles' sums of a column may differ.
+    const int own = int(tn) * 256;
+    const int m0 = min(int(tm) * 256, s.m - 256), n0 = min(own, s.n - 256);
 
     // a wave copies 64 tokens' rows and 64 of the matrix's, eight at a time
     const char *lds_x = smem, *lds_w = smem + 2 * 256 * 128, *lds_s = smem + 4 * 256 * 128;
@@ -333,8 +336,9 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
     for (int i = 0; i < 8; i += 2) copy_w(0, 0, i);
     copy_s(0, 0);
     if constexpr (std::is_same_v<X, f16>) {
-        // whether float16 holds the tile's rows: a thread looks at one row's scales
-        const uint8_t *row = scales + int64_t(n0 + int(threadIdx.x)) * ld_scales;
+        // whether float16 holds the tile's own rows: a thread looks at one row's scales
+        const int at = own + int(threadIdx.x);
+        const uint8_t *row = scales + int64_t(min(at, s.n - 1)) * ld_scales;
         bool fine = true;
 #pragma unroll 8
         for (int i = 0; i < s.k / kBlock; i += 4) {
@@ -352,7 +356,7 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
     asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");  // as settle() does
     pin(acc);
     __syncthreads();  // no copy is on its way when the block ends
-    store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane);
+    store_tile<TW>(acc, out, ld_out, m0 + wm, n0 + wn, s.m, s.n, lane, own);
 }
 
 // The gradient: dx[m][c] = sum over n of dy[m][n] w[n][c], 256 tokens by 256 columns, 64 rows n a step. The tokens'

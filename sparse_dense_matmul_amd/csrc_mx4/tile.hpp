@@ -173,10 +173,10 @@ struct Codes {
     }
 };
 
-// Results to out: out[m][n .. n + 3] for each run of four.
+// Results to out: out[m][n .. n + 3] for each run of four; columns before `from` are another tile's.
 template <int TW, typename O>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TW][TW], O *out, int64_t ld, int m0, int n0, int m, int n,
-                                           int lane) {
+                                           int lane, int from = 0) {
     using V = Vec<O, 4>;
 #pragma unroll
     for (int j = 0; j < TW; ++j) {
@@ -191,12 +191,12 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[TW][TW], O *out, 
                 V v;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = rounded<O>(acc[i][j][4 * q + e]);
-                if (nn + 4 <= n) {
+                if (nn + 4 <= n && nn >= from) {
                     *reinterpret_cast<V *>(row + nn) = v;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (nn + e < n) row[nn + e] = v[e];
+                        if (nn + e < n && nn + e >= from) row[nn + e] = v[e];
                 }
             }
     }
