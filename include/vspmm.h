@@ -645,9 +645,7 @@ vspmm_status vspmm_mx4_dequantize(vspmm_elt elt, int64_t rows, int64_t width, co
                                   void *out, int64_t ld_out, hipStream_t stream);
 
 /* out (m x n) = x (m x width, dense) times the transpose of w (n x width). x and
- * out are of elt. float16: a value of a block of scale 2^-87 or less, which no
- * float16 sum can show, may count as zero, also against an infinity (NaN).
- * Errors: as vspmm_mx4_quantize. */
+ * out are of elt. Errors: as vspmm_mx4_quantize. */
 vspmm_status vspmm_mx4_matmul(vspmm_elt elt, int64_t m, int64_t n, int64_t width, const void *x,
                               int64_t ld_x, const vspmm_mx4 *w, void *out, int64_t ld_out,
                               hipStream_t stream);

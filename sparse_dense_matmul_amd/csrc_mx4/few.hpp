@@ -178,7 +178,10 @@ __device__ __forceinline__ f32x4 multiply_step(i32x4 a, const Step<X> &x, f32x4 
 }
 
 // Whether a wave's chunk of a matrix may meet its tokens in float16: each lane answers for the block it loaded.
-__device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) { return __all(f16_scale(w.scale >> (8 * g) & 255)); }
+__device__ __forceinline__ bool f16_holds(const Piece<Mx4> &w, int g) {
+    const uint32_t b = w.scale >> (8 * g) & 255;
+    return __all(f16_scale(b) || f16_zeros(b, w.codes));
+}
 
 // acc += rows times tokens over the chunks [c0, c1) of a contraction of `width` values, U at a time. One tile's tokens are
 // loaded by chunks; those of several, which would need more registers than there are, and those in LDS beside the
@@ -352,7 +355,8 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[R][MT], const Row<W> (&r
                     for (int i = 0; i < R; ++i) {
                         word[n][i] = here ? word[n][i] : 0;
                         top[n][i] = here ? top[n][i] : 127;
-                        if constexpr (std::is_same_v<V, f16>) exact = exact && f16_scale(top[n][i]);
+                        if constexpr (std::is_same_v<V, f16>)
+                            exact = exact && (f16_scale(top[n][i]) || f16_zeros(top[n][i], word[n][i]));
                     }
                 }
                 if constexpr (Plain<X>::staged || std::is_same_v<V, Planes>) {

@@ -339,14 +339,19 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
         // whether float16 holds the tile's own rows: a thread looks at one row's scales
         const int at = own + int(threadIdx.x);
         const uint8_t *row = scales + int64_t(min(at, s.n - 1)) * ld_scales;
-        bool fine = true;
+        const uint8_t *row_codes = codes + int64_t(min(at, s.n - 1)) * ld_codes;
+        const bool holds = f16_holds([&](auto &&ok) {
+            bool fine = true;
 #pragma unroll 8
-        for (int i = 0; i < s.k / kBlock; i += 4) {
-            const uint32_t v = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(row + i);
+            for (int i = 0; i < s.k / kBlock; i += 4) {
+                const uint32_t v = *reinterpret_cast<const uint32_t __attribute__((aligned(1))) *>(row + i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) fine = fine && f16_scale(v >> (8 * e) & 255);
-        }
-        if (__syncthreads_and(fine)) run(f16{});
+                for (int e = 0; e < 4; ++e)
+                    fine = fine && ok(v >> (8 * e) & 255, row_codes + int64_t(i + e) * kBlockBytes);
+            }
+            return fine;
+        });
+        if (holds) run(f16{});
         else run(bf16{});
     } else {
         __syncthreads();
@@ -491,12 +496,17 @@ __global__ __launch_bounds__(256, 1) void k_stream_grad(const X *__restrict__ dy
     if constexpr (std::is_same_v<X, f16>) {
         // whether float16 holds the tile's columns: a thread looks at a block of every 32nd row
         const int b = c0 / kBlock + (tid & 7);
-        bool fine = true;
-        if (b < int(blocks_of_width(s.n))) {
+        const bool holds = f16_holds([&](auto &&ok) {
+            bool fine = true;
+            if (b < int(blocks_of_width(s.n))) {
 #pragma unroll 8
-            for (int row = tid >> 3; row < s.k; row += 32) fine = fine && f16_scale(scales[int64_t(row) * ld_scales + b]);
-        }
-        if (__syncthreads_and(fine)) run(f16{});
+                for (int row = tid >> 3; row < s.k; row += 32)
+                    fine = fine && ok(scales[int64_t(row) * ld_scales + b],
+                                      codes + int64_t(row) * ld_codes + b * kBlockBytes);
+            }
+            return fine;
+        });
+        if (holds) run(f16{});
         else run(bf16{});
     } else {
         run(bf16{});

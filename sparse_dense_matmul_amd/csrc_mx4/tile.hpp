@@ -321,12 +321,16 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile(const X *__restrict__
     if constexpr (std::is_same_v<X, f16>) {
         // float16 tokens meet the rows in float16 where it holds the tile's, else in two bfloat16 parts in bfloat16: the
         // block's threads share the rows' scales
-        bool fine = true;
         const int rows = min(EDGE, s.n - n0);
+        const bool holds = f16_holds([&](auto &&ok) {
+            bool fine = true;
 #pragma unroll 4
-        for (int64_t i = threadIdx.x; i < int64_t(rows) * blocks; i += kTileThreads * KS)
-            fine = fine && f16_scale(scales[(n0 + i / blocks) * ld_scales + i % blocks]);
-        if (__syncthreads_and(fine)) run(f16{});
+            for (int64_t i = threadIdx.x; i < int64_t(rows) * blocks; i += kTileThreads * KS)
+                fine = fine && ok(scales[(n0 + i / blocks) * ld_scales + i % blocks],
+                                  codes + (n0 + i / blocks) * ld_codes + i % blocks * kBlockBytes);
+            return fine;
+        });
+        if (holds) run(f16{});
         else run(bf16{});
     } else {
         run(bf16{});
@@ -436,13 +440,17 @@ __global__ __launch_bounds__(kTileThreads *KS) void k_tile_grad(const X *__restr
     if constexpr (std::is_same_v<X, f16>) {
         // whether float16 holds the tile's columns: the block's threads share their scales
         constexpr int TOPS = EDGE / kBlock;
-        bool fine = true;
+        const bool holds = f16_holds([&](auto &&ok) {
+            bool fine = true;
 #pragma unroll 4
-        for (int64_t i = threadIdx.x; i < int64_t(s.k) * TOPS; i += kTileThreads * KS) {
-            const int b = c0 / kBlock + int(i % TOPS);
-            fine = fine && (b >= blocks || f16_scale(scales[i / TOPS * ld_scales + b]));
-        }
-        if (__syncthreads_and(fine)) run(f16{});
+            for (int64_t i = threadIdx.x; i < int64_t(s.k) * TOPS; i += kTileThreads * KS) {
+                const int b = c0 / kBlock + int(i % TOPS);
+                fine = fine && (b >= blocks || ok(scales[i / TOPS * ld_scales + b],
+                                                  codes + i / TOPS * ld_codes + b * kBlockBytes));
+            }
+            return fine;
+        });
+        if (holds) run(f16{});
         else run(bf16{});
     } else {
         run(bf16{});
