@@ -16,6 +16,7 @@ namespace {
 constexpr int64_t kI32Max = 2147483647;
 constexpr int64_t kRowsMax = 1 << 30;   // rows of an array: the kernels' row numbers run past the end by a tile
 constexpr int64_t kWidthMax = 1 << 24;  // elements of a row
+constexpr int64_t kThreadsMax = 0xffffffff;  // threads of a launch along x: more are refused by the runtime
 
 vspmm_status launched() { return hipGetLastError() == hipSuccess ? VSPMM_OK : VSPMM_ERR_HIP; }
 

@@ -84,8 +84,11 @@ vspmm_status zero_rows(O *out, int64_t ld, int64_t rows, int64_t width, hipStrea
     return launched();
 }
 
-// Tiles of a product past one launch are of more than 2^43 results.
-bool too_many(int64_t m, int64_t n) { return ((m + 63) / 64) * ((n + 63) / 64) > kI32Max; }
+// Whether tiles of 128, taken for any large product, are more than one launch has threads for: 2^24 of them, whose results
+// are up to 2^38. (Few tokens take fewer blocks: the result's rows are of 2^24 values at most.)
+bool too_many(int64_t m, int64_t n) {
+    return ((m + 127) / 128) * ((n + 127) / 128) > kThreadsMax / kTileThreads;
+}
 
 // The few-token kernel, which reads the tokens once for 32 rows, takes up to 32 tokens, and dense ones up to 64 where its
 // blocks of 32 x 32 find a compute unit each (64 tokens through 4,096 x 4,096: 12.4 us, by tiles 17.6; 2,048 x 8,192: 23
@@ -165,10 +168,14 @@ vspmm_status vspmm_mx4_quantize(vspmm_elt elt, int32_t transpose, int64_t rows, 
         const T *p = static_cast<const T *>(x);
         if (transpose) {
             const int64_t col_tiles = (width + kTransposeCols - 1) / kTransposeCols;
-            const int64_t tiles = col_tiles * ((blocks + kTransposeWaves - 1) / kTransposeWaves);
-            if (tiles > kI32Max) return VSPMM_ERR_UNSUPPORTED;
-            hipLaunchKernelGGL(k_quantize_transposed<T>, dim3(unsigned(tiles)), dim3(64 * kTransposeWaves), 0, stream, p, ld_x,
-                               int(rows), int(width), int(blocks), uint32_t(col_tiles), codes, scales);
+            const int64_t row_tiles = (blocks + kTransposeWaves - 1) / kTransposeWaves;
+            const int64_t most = kThreadsMax / (64 * kTransposeWaves) / col_tiles;
+            for (int64_t first = 0; first < row_tiles; first += most) {
+                const int64_t tiles = col_tiles * std::min(most, row_tiles - first);
+                hipLaunchKernelGGL(k_quantize_transposed<T>, dim3(unsigned(tiles)), dim3(64 * kTransposeWaves), 0, stream,
+                                   p, ld_x, int(rows), int(width), int(blocks), int(first), uint32_t(col_tiles), codes,
+                                   scales);
+            }
             return launched();
         }
         const uint32_t per_row = uint32_t(4 * blocks);

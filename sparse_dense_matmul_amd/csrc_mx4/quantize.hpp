@@ -65,13 +65,13 @@ __global__ __launch_bounds__(256) void k_quantize(const T *__restrict__ x, int64
 constexpr int kTransposeWaves = 8, kTransposeCols = 128;
 template <typename T>
 __global__ __launch_bounds__(64 * kTransposeWaves) void k_quantize_transposed(
-    const T *__restrict__ x, int64_t ld, int rows, int width, int blocks, uint32_t col_tiles,
+    const T *__restrict__ x, int64_t ld, int rows, int width, int blocks, int first_tile, uint32_t col_tiles,
     uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     // a column's blocks, 16 bytes further for every column so that the lanes' stores spread over the banks
     __shared__ i32x4 tile[kTransposeCols][kTransposeWaves + 1];
     __shared__ uint8_t tops[kTransposeCols][kTransposeWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int b0 = int(blockIdx.x / col_tiles) * kTransposeWaves;
+    const int b0 = (first_tile + int(blockIdx.x / col_tiles)) * kTransposeWaves;
     const int col0 = int(blockIdx.x % col_tiles) * kTransposeCols, col = col0 + 2 * lane;
     const int64_t r0 = int64_t(b0 + wave) * kBlock;
     const T *p = x + r0 * ld + col;
