@@ -261,7 +261,8 @@ vspmm_status vspmm_mx4_matmul_grad(vspmm_elt elt, int64_t m, int64_t n, int64_t 
         using T = decltype(e);
         T *o = static_cast<T *>(grad);
         if (n == 0) return zero_rows(o, ld_grad, m, width, stream);
-        if (m >= 256 && n % kStepHalf == 0 && fill(m, width) && streams(dout, ld_dout)) {
+        // (a wave's copies of 64 rows reach 2^31 bytes past the first)
+        if (m >= 256 && n % kStepHalf == 0 && fill(m, width) && streams(dout, ld_dout) && n + 64 * ld_dout <= 1 << 30) {
             unsigned tiles;
             const TileShape s = tile_shape(m, width, n, 256, tiles);
             allow_lds<&k_stream_grad<T>>(kStreamGradLds);
