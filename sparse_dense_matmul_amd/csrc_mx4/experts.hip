@@ -526,14 +526,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
     }
     if (from.splits == 1) return;
     // the last block to come adds all parts, in their order: each wave's stores are acknowledged before the barrier
-    __shared__ int s_last;
+    int *last = reinterpret_cast<int *>(smem);  // the sums are no longer needed
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0)
-        s_last = __hip_atomic_fetch_add(&from.arrived[group * from.tiles + int(blockIdx.x)], 1, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT) == from.splits - 1;
+        *last = __hip_atomic_fetch_add(&from.arrived[group * from.tiles + int(blockIdx.x)], 1, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT) == from.splits - 1;
     __syncthreads();
-    if (!s_last) return;
+    if (!*last) return;
     for (int i = threadIdx.x; i < count * 4; i += 64 * kDownWaves) {
         f32x4 sum = load_part(0, i);
         for (int z = 1; z < from.splits; ++z) sum += load_part(z, i);
@@ -643,7 +643,8 @@ void launch(const Choices &ch, const X *x, int64_t ld_x, const vspmm_expert_matr
         constexpr int MT = decltype(mt)::value;
         constexpr bool FEW = decltype(by_few)::value, STAGE = decltype(stage)::value;
         const size_t lds = size_t(kDownWaves) * std::min(ch.tokens, kGroup) * 64 + staged;
-        allow_lds<&k_experts_down<W, X, MT, FEW, STAGE>>(size_t(kDownWaves) * 16 * 64 + (STAGE ? 2 * kStageMax : 0));
+        allow_lds<&k_experts_down<W, X, MT, FEW, STAGE>>(size_t(kDownWaves) * (MT > 1 ? kGroup : 16) * 64 +
+                                                         (STAGE ? 2 * kStageMax : 0));
         hipLaunchKernelGGL((k_experts_down<W, X, MT, FEW, STAGE>),
                            dim3(b.tiles, b.groups, b.splits), dim3(64 * kDownWaves), lds, s, ch,
                            b, matrix<W>(down), hidden, width, out, ld_out);

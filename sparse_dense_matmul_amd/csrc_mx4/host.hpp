@@ -28,13 +28,14 @@ auto with_dense(int elt, F &&f) {
     return elt == VSPMM_ELT_BF16 ? f(bf16{}) : f(f16{});
 }
 
-// A kernel that may use more LDS than the default limit of 64 KB, up to `most` bytes, says so once for each device
-// (a call on the host of 1.7 us, where a launch takes 3).
+// A kernel that may use more LDS than the default limit of 64 KB, up to `most` bytes of its launch's and 1 KB of its own
+// (a vote of a block's threads has 256 bytes), says so once for each device (a call on the host of 1.7 us, where a launch
+// takes 3).
 template <auto Kernel>
 void allow_lds(size_t most) {
     static std::atomic<uint64_t> done{0};
     int device = 0;
-    if (most <= 64 * 1024 || hipGetDevice(&device) != hipSuccess) return;
+    if (most <= 63 * 1024 || hipGetDevice(&device) != hipSuccess) return;
     const uint64_t bit = uint64_t(1) << (device & 63);
     if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return;
     if (hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
