@@ -265,7 +265,10 @@ def expert_mlp(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor,
     weights = _weights(weights, (t, k), torch.float32, dev)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    shape = (gate.codes if isinstance(gate, Mx4) else gate).shape
+    shape = gate.codes if isinstance(gate, Mx4) else gate
+    if not isinstance(shape, torch.Tensor):
+        raise TypeError("gate must be a tensor or an Mx4")
+    shape = shape.shape
     if len(shape) != 3:
         raise ValueError(f"gate has shape {tuple(shape)}, expected (experts, hidden, width)")
     n, hidden = shape[0], shape[1]
