@@ -29,7 +29,8 @@ from typing import NamedTuple
 import torch
 
 from . import _check, lib
-from .selection import ELTS, _apart, _call, _index, _region, _rows, _weights, _workspace
+from .selection import (ELTS, _apart, _call, _index, _overlap, _region, _rows, _weights,
+                        _workspace)
 
 __all__ = ["Mx4", "dequantize_mx4", "expert_mlp", "expert_mlp_workspace", "matmul_mx4",
            "matmul_mx4_grad", "quantize_mx4"]
@@ -232,6 +233,22 @@ def _expert_matrix(t, name, like, shape, device):
     return _Expert(t.data_ptr(), t.stride(1), t.stride(0), None, 0, 0), False, (t,)
 
 
+def _experts_apart(name, written, matrices):
+    """_apart for arrays of every expert, as (name, tensor): one look at the bytes
+    from the first to the last, and at each expert's rows only if those overlap."""
+    for other, m in matrices:
+        if not m.numel():
+            continue
+        last = sum((n - 1) * stride for n, stride in zip(m.shape, m.stride()))
+        whole = (m.data_ptr(), 1, (last + 1) * m.element_size(), 0)
+        if not _overlap(written, whole):
+            continue
+        if m.is_contiguous():
+            _apart(name, written, **{other: whole})
+        for e in range(m.shape[0]):
+            _apart(name, written, **{f"{other}[{e}]": _region(m[e], m.stride(1))})
+
+
 def expert_mlp_workspace(n_tokens: int, top_k: int, n_experts: int, width: int,
                          hidden: int) -> int:
     """Workspace bytes of :func:`expert_mlp`."""
@@ -278,23 +295,23 @@ def expert_mlp(x: torch.Tensor, experts: torch.Tensor, weights: torch.Tensor,
     if mx4 != mx4_up or mx4 != mx4_down:
         raise TypeError("gate, up and down must all be in 4 bits, or none")
     need = expert_mlp_workspace(t, k, n, width, hidden)
-    read = None
+    read = matrices = None
     if out is not None or workspace is not None:
         read = {"x": _region(x, ld), "experts": _region(experts), "weights": _region(weights)}
-        for name, arrays in (("gate", a), ("up", b), ("down", c)):
-            for i, m in enumerate(arrays):
-                for e in range(n if not m.is_contiguous() else 1):
-                    part = _region(m) if m.is_contiguous() else _region(m[e], m.stride(1))
-                    read[f"{name}[{e}]" if len(arrays) == 1 else f"{name}[{e}], part {i}"] = part
+        matrices = [(name if len(arrays) == 1 else f"{name}.{part}", m)
+                    for name, arrays in (("gate", a), ("up", b), ("down", c))
+                    for part, m in zip(("codes", "scales"), arrays)]
     if out is None:
         out, ld_out = x.new_empty(t, width), width
     else:
         out, ld_out = _dense(out, "out", DENSE, (t, width), x.dtype, dev, write=True)
         _apart("out", _region(out, ld_out), **read)
+        _experts_apart("out", _region(out, ld_out), matrices)
     ws, ws_bytes = _workspace(need, workspace, dev)
     if workspace is not None:
-        _apart("workspace", (ws.data_ptr(), 1, min(need, ws_bytes), 0), out=_region(out, ld_out),
-               **read)
+        region = ws.data_ptr(), 1, min(need, ws_bytes), 0
+        _apart("workspace", region, out=_region(out, ld_out), **read)
+        _experts_apart("workspace", region, matrices)
     _call(dev, "vspmm_expert_mlp", lib.vspmm_expert_mlp, ELTS[x.dtype],
           ELT_MX4 if mx4 else ELTS[x.dtype], 0 if experts.dtype == torch.int32 else 1,
           ACTIVATIONS[activation], t, k, n, width, hidden, x.data_ptr(), ld, experts.data_ptr(),
