@@ -387,8 +387,8 @@ __global__ __launch_bounds__(256, 1) void k_stream_grad(const X *__restrict__ dy
 
     const int64_t ld_b = ld_dy * 2;
     const Buffer src = buffer_of(reinterpret_cast<const uint8_t *>(dy) + (m0 + 64 * wave) * ld_b);
-    const uint32_t off = uint32_t(lane >> 3) * uint32_t(ld_b) + 16 * ((lane & 7) ^ (lane >> 3));
-    const uint32_t offs[2] = {off, off ^ 16}, rows8 = 8 * uint32_t(ld_b);
+    const uint32_t off = uint32_t(lane >> 3) * uint32_t(ld_b), piece = 16 * ((lane & 7) ^ (lane >> 3));
+    const uint32_t offs[2] = {off + piece, off + (piece ^ 16)}, rows8 = 8 * uint32_t(ld_b);
     Lds *to = (Lds *)smem + wave * 64 * 128;
     auto copy = [&](int it, int buf, int i) {
         copy16(src, offs[i & 1], uint32_t(it) * 128 + i * rows8, to + buf * 256 * 128 + i * 1024);
