@@ -618,10 +618,15 @@ vspmm_status vspmm_combine_grad(vspmm_elt elt, int64_t n_tokens, int64_t top_k, 
  *
  * Conventions of these calls are those of the selection products. Dense
  * operands are VSPMM_ELT_BF16 or _F16 (also _F32 where said). Every product
- * multiplies its operands' exact values and sums in float32, in an order that
- * depends only on the sizes and types; results are rounded once. A value past
- * float32's (a scale byte above 252) counts as infinite. Extents of rows are at
- * most 2^30, widths at most 2^24 (_UNSUPPORTED above). */
+ * multiplies its operands' exact values and sums in float32; results are rounded
+ * once. Equal calls give equal bits: the order of a sum depends on the sizes, the
+ * types and the arrays' alignment, with float16 operands also on the scales of
+ * the 4-bit rows multiplied beside it, and in vspmm_expert_mlp on which experts
+ * are chosen. With a dense operand a value past float32's (4 and 6 at a scale
+ * byte of 253 or 254) counts as infinite; products of two 4-bit values are exact
+ * where float32 holds them. Extents of rows are at most 2^30, widths (a result's,
+ * too) at most 2^24, and a result has fewer than 2^24 tiles of 128 x 128
+ * (_UNSUPPORTED above). */
 typedef struct {
     const uint8_t *codes;  /* device */
     const uint8_t *scales; /* device */
@@ -680,15 +685,16 @@ typedef enum { VSPMM_SILU = 0, VSPMM_GELU = 1 } vspmm_activation;
  * or VSPMM_ELT_MX4. experts: device int32 or int64 [n_tokens, top_k]; a choice
  * outside [0, n_experts) adds nothing, and only the weights of experts that some
  * token chose are read. weight: device float32 [n_tokens, top_k]. act: x / (1 +
- * exp(-x)), or x / 2 (1 + erf(x / sqrt 2)). Sums, activations
- * and hidden values, which take the token's weight (the sum of its weights where
- * it chose an expert more than once), are in float32 (what a hidden value has
- * under 2^-133 is lost). An infinite or NaN weight, 4-bit value or hidden value
- * gives what float32 products with it give. A token's result does not depend on the
- * others' values. More tokens: vspmm_route, vspmm_dispatch, a product per expert
- * and vspmm_combine. ws: vspmm_expert_mlp_workspace_size bytes. Errors: _NULL,
- * _DIM, _ENUM, _WORKSPACE, _UNSUPPORTED (more than 1,024 tokens, 4,096 experts or
- * choices a token, or rows of more than 2^24), _HIP. */
+ * exp(-x)), or x / 2 (1 + erf(x / sqrt 2)). Sums, activations and hidden values,
+ * which take the token's weight (the sum of its weights where it chose an expert
+ * more than once), are in float32 (what a hidden value has under 2^-133 is lost).
+ * An infinite or NaN weight, 4-bit value or hidden value gives what float32
+ * products with it give. A token's result does not depend on the other tokens'
+ * values; the order of its sums depends on which experts they chose. More tokens:
+ * vspmm_route, vspmm_dispatch, a product per expert and vspmm_combine. ws:
+ * vspmm_expert_mlp_workspace_size bytes. Errors: _NULL, _DIM, _ENUM, _WORKSPACE,
+ * _UNSUPPORTED (more than 1,024 tokens, 4,096 experts or choices a token, or rows
+ * of more than 2^24), _HIP. */
 vspmm_status vspmm_expert_mlp(vspmm_elt elt, vspmm_elt weights_elt, vspmm_index index,
                               vspmm_activation activation, int64_t n_tokens, int64_t top_k,
                               int64_t n_experts, int64_t width, int64_t hidden, const void *x,

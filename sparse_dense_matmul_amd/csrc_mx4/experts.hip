@@ -8,8 +8,9 @@
 // last adds their parts, in order. Every sum's order is fixed. Hidden values go between the launches as the sum of three
 // bfloat16 numbers, which hold float32's 24 bits and which the second launch's matrix instructions take as they are.
 //
-// 64 tokens to 8 of 128 experts of 4,096 x 1,024, bfloat16: 417 and 235 us, 4.9 TB/s of weights. One token, 4 bits: 13
-// and 9 us, latency: 7.5 us of bytes.
+// 64 tokens to 8 of 128 experts of 4,096 x 1,024, bfloat16: 419 and 267 us, 5.0 and 3.9 TB/s of weights; the second is
+// bound by the hidden values, which every 16 columns read again, 6 bytes each (two parts of 17 bits: 235 us). One token, 4
+// bits: 14 and 10 us, latency: 7.5 us of bytes.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -382,7 +383,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_experts_down(Choices ch, Be
     f32x4 *own = sums + wave * count * 4;
     for (int i = lane; i < count * 4; i += 64) own[i] = f32x4{};
     using H = std::conditional_t<STAGE, Staged<Planes>, Planes>;
-    // chunks on their way at once: one of hidden values and 16-bit weights takes 64 registers
+    // Chunks on their way at once. One of hidden values and 16-bit weights takes 64 registers, and with two no second block
+    // fits a unit (1,024 tokens to 2 of 8 experts of 2,048 x 1,408 in 587 us for 526, 64 to 8 of 128 in 677 for 676); with
+    // 4-bit weights two take 410 us, one 425, four 413.
     constexpr int AT_ONCE = !STAGE ? (std::is_same_v<W, Mx4> ? 2 : 1) : std::is_same_v<W, f16> ? 2 : 4;
     bf16 *staged = reinterpret_cast<bf16 *>(sums + kDownWaves * count * 4);
     const int slots = ch.tokens * ch.top_k, row = staged_planes(hidden);

@@ -147,8 +147,10 @@ __device__ __forceinline__ f32x16 mma32_mx4(i32x4 a, uint32_t sa, i32x4 b, uint3
 
 // Waits until the matrix instructions have written their sums. The compiler puts waits between such an instruction and
 // a use of its result, but here it was seen to leave them out: where a branch leads past a short block straight from
-// the instruction to the use, the first registers of the sum were read too early. So the products have no branches
-// between them that depend on data, and a sum goes through here before any use but another product.
+// the instruction to the use, the first registers of the sum were read too early. So a sum goes through here before any
+// use but another product. Branches between products (float16 tokens choose their type at every chunk, the last chunks go
+// by size) lead from products to products on the same sums, or to here. In the assembly of every kernel, along every
+// path, no other instruction reads a product's result before 8 wait states (16 x 16) or 12 (32 x 32).
 template <typename V, int A, int B>
 __device__ __forceinline__ void settle(V (&acc)[A][B]) {
 #pragma unroll

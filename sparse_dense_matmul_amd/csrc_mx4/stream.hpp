@@ -69,9 +69,9 @@ __device__ __forceinline__ void mix_widening() {
 }
 
 // Both sides in 4 bits: a step is 256 codes, 128 bytes of a row of each side. One wave a SIMD holds 128 x 128 results, so
-// that a step's 64 products need 16 loads from LDS; smaller tiles read as much for a quarter of the products. Bound by
-// the clock that the card holds under the matrix instructions: 8,192^3 in 309 to 323 us, 3.4 to 3.6 PFLOP/s, where they
-// alone reach 6.5 on random codes.
+// that a step's 64 products need 16 loads from LDS; smaller tiles read as much for a quarter of the products. 8,192^3 in
+// 308 to 333 us, 3.3 to 3.6 PFLOP/s, where the instructions alone reach 6.5 on random codes. Every step waits for all of
+// its copies at its barrier, whose last ones leave 12 products before it; what the waits cost was not told apart.
 constexpr int kStreamEdge = 256;
 constexpr size_t kStreamBothLds = 2 * 512 * (128 + 16);
 
@@ -205,7 +205,8 @@ __global__ __launch_bounds__(256, 1) void k_stream_both(const uint8_t *__restric
 // Dense tokens. A step is 64 values: 128 bytes of a token's row, copied for every step, and a quarter of the 128 bytes
 // of codes of a row, copied for every four. An instruction's part of the rows is widened while the part before it is
 // multiplied. Bound by the clock under the matrix instructions and by what the conversions take beside them: 4,096 tokens
-// through 8,192 x 8,192 in 407 to 467 us, 1.18 to 1.35 PFLOP/s (1.7 by the instructions alone on random operands).
+// through 8,192 x 8,192 in 405 to 467 us, 1.18 to 1.36 PFLOP/s (1.7 by the instructions alone on random operands); float16
+// 434 to 450 us.
 constexpr size_t kStreamLds = 2 * 256 * (128 + 128 + 16);
 
 template <typename X>
@@ -368,7 +369,8 @@ __global__ __launch_bounds__(256, 1) void k_stream(const X *__restrict__ x, int6
 // rows are copied as above. The matrix's codes go through registers: a thread takes eight columns of eight rows, a word
 // from each, widens them, joins pairs of rows and writes each column's eight values to its row in LDS. A step's words
 // are loaded a step ahead of that. Bound as above, with the columns' stores to LDS: 4,096 tokens, 8,192 rows of 4,096 in
-// 221 to 235 us, 1.17 to 1.24 PFLOP/s.
+// 219 to 236 us, 1.16 to 1.26 PFLOP/s. float16 gradients 287 to 298 us: a look at the columns' scales comes first, one after
+// another.
 constexpr size_t kStreamGradLds = 2 * 256 * (128 + 128);
 
 template <typename X>
